@@ -417,6 +417,122 @@ ssd_status ssd_backward(const ssd_shape* shape, const void* x, const float* a, c
  * invalid or not served (a_per_state with N > 128). */
 size_t ssd_backward_workspace_size(const ssd_shape* shape);
 
+/* ---- linear attention with a decay for each head -------------------------- */
+
+/* The sequence mixer whose state decays by one fixed number per head:
+ *     h_t = exp(decay[h]) h_{t-1} + k_t v_t^T,     y_t = scale q_t^T h_t
+ * i.e. the operator above with one log-decay for all tokens of a head and no
+ * skip term ("State Space Duality", aiwiki: the duality with causal linear
+ * attention, q = C, k = B, v = x), in the forms its users have it: keys and
+ * values shared by the query heads of a group, q, k, v as slices of one
+ * projection, sequences of different lengths packed one behind the other.
+ *
+ *   q [B][T][H][K], k [B][T][G][K], v [B][T][G][V]   dtype; head h of q reads
+ *       head h / (H/G) of k and v.  The last dimension is contiguous, the
+ *       others as the strides (in elements) say; NULL strides = contiguous.
+ *       No alignment beyond the element's is needed.
+ *   decay [H] fp32 log-decays (<= 0 assumed, not checked)
+ *   y [B][T][H][V] dtype, contiguous
+ *   states [B][H][K][V] fp32, contiguous: the layout of ssd_forward's states
+ * packed != 0: the tensors have no batch dimension ([T][heads][d]); sequence s
+ * of the B sequences is the rows cu_seqlens[s] <= t < cu_seqlens[s+1]
+ * (cu_seqlens [B+1] int32 on the device, never decreasing, within [0, T];
+ * a sequence may be empty: its final state is then its initial state).  Rows
+ * outside every sequence are neither read nor written.  Offsets that break
+ * these rules are clamped into [0, T]: the results are then undefined, but
+ * nothing outside the buffers is touched.
+ * Requirements: all sizes >= 1, G divides H, K <= 256, V <= 256; at most
+ * 2^31 / 12 (sequence, head) pairs. */
+typedef struct {
+    int B, T, H, G, K, V;
+    int dtype;  /* ssd_dtype of q, k, v and y */
+    int packed; /* 0: rows [B][T]; 1: rows [T] of B sequences, see cu_seqlens */
+} ssd_linear_shape;
+
+typedef struct {
+    long long batch, token, head; /* in elements; batch is unused when packed */
+} ssd_strides;
+
+/* The whole sequences: y, and the state after each sequence's last token
+ * (final_state, NULL = not wanted) from the state before its first
+ * (initial_state, NULL = zero; may alias final_state).  cu_seqlens is NULL
+ * unless packed.  workspace: device, >= ssd_linear_workspace_size bytes,
+ * 256-byte aligned; its first word is a status for ssd_device_status(), as
+ * for ssd_forward; not to be shared by calls that overlap in time (captured
+ * graphs that replay side by side need one each).  bf16 with K, V <= 128, K
+ * and V multiples of 8 and rows on 16-byte boundaries (addresses, and
+ * strides multiples of 8) runs on tensor cores: the masked scores and the
+ * state as an operand are rounded to bf16, sums and states are fp32.
+ * Everything else runs on CUDA cores in fp32.  Asynchronous on `stream`. */
+ssd_status ssd_linear_attention(const ssd_linear_shape* shape, const void* q, const ssd_strides* q_strides,
+                                const void* k, const ssd_strides* k_strides, const void* v,
+                                const ssd_strides* v_strides, const float* decay, const int* cu_seqlens,
+                                const float* initial_state, float scale, void* y, float* final_state,
+                                void* workspace, size_t ws_bytes, ssd_stream stream);
+
+/* Bytes of workspace ssd_linear_attention needs for this shape, 0 when the
+ * shape is invalid. */
+size_t ssd_linear_workspace_size(const ssd_linear_shape* shape);
+
+/* One token for a batch of sequences (shape: T == 1, not packed), the state
+ * [B][H][K][V] updated in place: h <- exp(decay) h + k v^T, y = scale q^T h.
+ * Continues the final state of ssd_linear_attention. */
+ssd_status ssd_linear_attention_step(const ssd_linear_shape* shape, const void* q, const ssd_strides* q_strides,
+                                     const void* k, const ssd_strides* k_strides, const void* v,
+                                     const ssd_strides* v_strides, const float* decay, float scale, float* state,
+                                     void* y, ssd_stream stream);
+
+/* Gradients of sum(dy . y) + <dfinal, final_state> for the same inputs:
+ *     dq_t = scale h_t dy_t,  G_t = exp(decay) G_{t+1} + scale q_t dy_t^T
+ *     (G at the last token: dfinal + scale q dy^T),  dk_t = G_t v_t,
+ *     dv_t = G_t^T k_t,  dinit = exp(decay) G_0 (dfinal for an empty sequence)
+ * The decay is a constant of the layer and has no gradient here.
+ *   dy [B][T][H][V] dtype, contiguous; dfinal, dinit [B][H][K][V] fp32 or NULL
+ *   dq [B][T][H][K], dk [B][T][G][K], dv [B][T][G][V] dtype, contiguous; dk and
+ *   dv are summed over the query heads of a group (in fp32, in a fixed order)
+ * scale must not be 0.  Rows outside every packed sequence: dq is left as it
+ * is; dk and dv too when H == G, undefined otherwise. */
+ssd_status ssd_linear_attention_backward(const ssd_linear_shape* shape, const void* q, const ssd_strides* q_strides,
+                                         const void* k, const ssd_strides* k_strides, const void* v,
+                                         const ssd_strides* v_strides, const float* decay, const int* cu_seqlens,
+                                         const float* initial_state, float scale, const void* dy, const float* dfinal,
+                                         void* dq, void* dk, void* dv, float* dinit, void* workspace,
+                                         size_t ws_bytes, ssd_stream stream);
+size_t ssd_linear_backward_workspace_size(const ssd_linear_shape* shape);
+
+/* ---- layer norm, by rows or by heads, with an optional gate ---------------- */
+
+/* Over each of the `groups` equal parts of a row (one part: layer norm; one
+ * part per head: the norm behind a sequence mixer):
+ *     xh = (x - mean) rstd,  rstd = (var + eps)^(-1/2),  y = (xh weight + bias) silu(gate)
+ * x [rows][width] dtype with x_stride elements from row to row; gate the same
+ * with gate_stride, or NULL (no product); weight, bias [width] fp32 or NULL (1
+ * and 0); y [rows][width] dtype, contiguous; stats [rows][groups][2] fp32, mean
+ * and rstd, or NULL (not wanted; the backward needs it).  width / groups <=
+ * 16384; eps > 0.  Statistics are fp32, the variance taken about the mean. */
+typedef struct {
+    long long rows;
+    int width, groups;
+    int dtype; /* ssd_dtype of x, gate and y */
+} ssd_norm_shape;
+
+ssd_status ssd_layer_norm(const ssd_norm_shape* shape, const void* x, long long x_stride, const float* weight,
+                          const float* bias, const void* gate, long long gate_stride, float eps, void* y,
+                          float* stats, ssd_stream stream);
+
+/* Gradients of sum(dy . y): dx, dgate (dtype, contiguous; dgate given exactly
+ * when gate is) and dweight, dbias [width] fp32 (either may be NULL), added
+ * over the rows in a fixed order.  dy with dy_stride elements from row to row;
+ * stats as ssd_layer_norm wrote them.  workspace: >=
+ * ssd_layer_norm_backward_workspace_size bytes, 256-byte aligned (unused, and
+ * may be NULL, when neither dweight nor dbias is wanted). */
+ssd_status ssd_layer_norm_backward(const ssd_norm_shape* shape, const void* x, long long x_stride,
+                                   const float* weight, const float* bias, const void* gate,
+                                   long long gate_stride, const void* dy, long long dy_stride, const float* stats,
+                                   void* dx, float* dweight, float* dbias, void* dgate, void* workspace,
+                                   size_t ws_bytes, ssd_stream stream);
+size_t ssd_layer_norm_backward_workspace_size(const ssd_norm_shape* shape);
+
 /* ---- the debug build's index checks ---------------------------------------
  * The library also comes as a debug build (libssd_debug.so, compiled with
  * SSD_DEBUG_CHECKS; the Python binding loads it when the environment variable

@@ -1,4 +1,7 @@
-"""PyTorch autograd for the chunked SSD forward: y, final = ssd_autograd(...)
+"""PyTorch autograd for the chunked SSD forward, linear attention with a decay
+for each head and layer norm.
+
+The chunked SSD forward: y, final = ssd_autograd(...)
 takes part in a torch graph, and its backward is the library's ssd_backward
 (the gradients of sum(dy * y) + <dfinal, final> that autograd asks for).
 
@@ -54,3 +57,68 @@ def ssd_autograd(x, a, Bm, Cm, D=None, chunk=256, initial_state=None, *, ops=Non
     Shapes and dtypes as for ssd.forward; gradients flow to x, a, Bm, Cm, D
     and initial_state (whichever require them)."""
     return SSDFunction.apply(x, a, Bm, Cm, D, initial_state, chunk, ops or _Ops)
+
+
+class _LinearOps:
+    forward = staticmethod(ssd.linear_attention)
+    backward = staticmethod(ssd.linear_attention_backward)
+
+
+class LinearAttentionFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, decay, initial_state, cu_seqlens, scale, ops):
+        y, final = ops.forward(q, k, v, decay, scale=scale, initial_state=initial_state, cu_seqlens=cu_seqlens)
+        ctx.save_for_backward(q, k, v, decay, initial_state, cu_seqlens)
+        ctx.scale, ctx.ops = scale, ops
+        ctx.set_materialize_grads(False)
+        return y, final
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dfinal):
+        q, k, v, decay, init, cu = ctx.saved_tensors
+        if dy is None:
+            dy = q.new_zeros(q.shape[:-1] + v.shape[-1:])
+        want = init is not None and ctx.needs_input_grad[4]
+        g = ctx.ops.backward(q, k, v, decay, dy.contiguous(), scale=ctx.scale, initial_state=init,
+                             dfinal=None if dfinal is None else dfinal.contiguous(), cu_seqlens=cu, want_dinit=want)
+        return g["dq"], g["dk"], g["dv"], None, g["dinit"] if want else None, None, None, None
+
+
+def linear_attention_autograd(q, k, v, decay, *, scale=None, initial_state=None, cu_seqlens=None, ops=None):
+    """(y, final_state) of ssd.linear_attention as a differentiable torch
+    operation; gradients flow to q, k, v and initial_state.  The decay is a
+    constant of the layer: one that requires a gradient is refused (a learned
+    log-decay per token is what ssd_autograd takes)."""
+    if decay.requires_grad:
+        raise ValueError("decay has no gradient here; use ssd_autograd for a learned decay")
+    return LinearAttentionFunction.apply(q, k, v, decay, initial_state, cu_seqlens, scale, ops or _LinearOps)
+
+
+class _NormOps:
+    forward = staticmethod(ssd.layer_norm)
+    backward = staticmethod(ssd.layer_norm_backward)
+
+
+class LayerNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, gate, groups, eps, ops):
+        y, stats = ops.forward(x, weight, bias, groups=groups, gate=gate, eps=eps)
+        ctx.save_for_backward(x, weight, bias, gate, stats)
+        ctx.groups, ctx.ops = groups, ops
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, weight, bias, gate, stats = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        g = ctx.ops.backward(x, weight, bias, dy.contiguous(), stats, groups=ctx.groups, gate=gate,
+                             want_dweight=weight is not None and need[1], want_dbias=bias is not None and need[2])
+        return g["dx"], g["dweight"], g["dbias"], g["dgate"], None, None, None
+
+
+def layer_norm_autograd(x, weight=None, bias=None, *, groups=1, gate=None, eps=1e-5, ops=None):
+    """y of ssd.layer_norm as a differentiable torch operation; gradients flow
+    to x, weight, bias and gate."""
+    return LayerNormFunction.apply(x, weight, bias, gate, groups, eps, ops or _NormOps)

@@ -1,0 +1,372 @@
+// linear_simt.cu -- the linear-attention scan on CUDA cores (fp32 arithmetic,
+// any sizes up to 256, any strides), the combination of the states of cut
+// chains, and the sum of a shared head's gradients over its query heads.
+//
+// One block per (item, 64 columns of the state).  Chunks of 32 tokens: with
+// positions i, j in the chunk, n tokens in it, H the state entering it and
+// l = exp(decay),
+//     out_i = sum_{j<=i} l^(i-j) (q_i.k_j) v_j + l^(i+1) q_i^T H
+//     H    <- l^n H + sum_j l^(n-1-j) k_j v_j^T
+// and the mirror image of it for a scan backwards.  The chunk's rows and H are
+// in shared memory as fp32; every product is a small register tile.  32 tokens
+// keep the masked quadratic part small next to the two state products, which
+// are the operator's own work (2 K V multiply-adds per token and head).
+#include "../common.cuh"
+#include "../debug_checks.cuh"
+#include "../linear.h"
+
+namespace ssd {
+namespace {
+
+constexpr int kC = 32;        // tokens of a chunk
+constexpr int kVT = 64;       // state columns of a block
+constexpr int kThreads = 256;
+
+struct SimtLayout {
+    int K4, ldk;  // K rounded up to 4, row pitch of q and k
+    size_t bytes;
+};
+__host__ __device__ inline SimtLayout simt_layout(int K) {
+    SimtLayout l;
+    l.K4 = (K + 3) & ~3;
+    l.ldk = l.K4 + 4;  // rows start 4 banks apart: eight rows' 16-byte reads meet no bank twice
+    l.bytes = (size_t)(2 * kC * l.ldk + kC * kVT + kC * (kC + 4) + l.K4 * kVT + kC + 4) * sizeof(float);
+    return l;
+}
+
+// rows [t, t+n) of a tensor, D of its columns from c0 on, into fp32 rows of
+// pitch ld; the rows behind n and the columns behind D up to Dp are zero
+template <typename T>
+__device__ void load_rows(const RowTensor& a, const ScanItem& it, int t, int n, int c0, int D, int Dp, int ld,
+                          float* dst, long long rows, long long batches) {
+    const T* base = (const T*)a.p + (long long)it.batch * a.batch + (long long)(it.head / a.share) * a.head + c0;
+    for (int e = threadIdx.x; e < kC * Dp; e += kThreads) {
+        const int r = e / Dp, c = e - r * Dp;
+        float v = 0.f;
+        const long long row = it.row0 + t + r;
+        if (r < n && c < D && SSD_INB(row, rows) && SSD_INB(it.batch, batches)) v = to_f32(base[row * a.token + c]);
+        dst[r * ld + c] = v;
+    }
+}
+
+template <typename T, bool kOut>
+__global__ void __launch_bounds__(kThreads) scan_simt_kernel(const ScanLaunch p, int ntiles) {
+    extern __shared__ __align__(16) float sm[];
+    __shared__ ScanItem sItem;
+    if (p.reset && blockIdx.x == 0 && threadIdx.x == 0) *p.status = kDevOk;
+    if (threadIdx.x < 32) {
+        ScanItem it = scan_item(p.plan, blockIdx.x / ntiles);
+        if (it.valid) scan_item_tokens(it, p.plan.seg_tokens, p.role[it.role].reverse);
+        if (threadIdx.x == 0) sItem = it;
+    }
+    __syncthreads();
+    const ScanItem it = sItem;
+    if (!it.valid || (!kOut && it.seg == it.nseg - 1)) return;
+    const ScanRole& R = p.role[it.role];
+    const int K = R.K, V = R.V, H = p.plan.H;
+    const int v0 = (blockIdx.x % ntiles) * kVT;
+    if (v0 >= V) return;
+    const int vn = min(kVT, V - v0);
+    const SimtLayout L = simt_layout(K);
+    float* sQ = sm;
+    float* sK = sQ + kC * L.ldk;
+    float* sV = sK + kC * L.ldk;            // [kC][kVT]
+    float* sP = sV + kC * kVT;              // [kC][kC + 4]
+    float* sH = sP + kC * (kC + 4);         // [K4][kVT]
+    float* sTab = sH + L.K4 * kVT;          // l^0 .. l^kC
+    const int tid = threadIdx.x;
+    const float la = p.decay[it.head];
+    for (int d = tid; d <= kC; d += kThreads) sTab[d] = decay_power(la, d).x;
+    const long long rows = p.plan.T, batches = p.plan.packed ? 1 : p.plan.B;
+    (void)batches;
+    const long long chain = (long long)it.seq * H + it.head;
+    const long long chains = (long long)p.plan.B * H;
+
+    // the state entering the item
+    const bool from_init = it.seg == 0;
+    for (int e = tid; e < L.K4 * kVT; e += kThreads) {
+        const int k = e / kVT, c = e % kVT;
+        float h = 0.f;
+        if (kOut && k < K && c < vn) {
+            if (!from_init) {
+                const long long at = it.slot_prev * K * V + (long long)k * V + v0 + c;
+                if (SSD_INB(at, p.plan.slots() * K * V)) h = p.states[at];
+            } else if (R.init) {
+                const long long at = chain * K * V + k * R.init_k + (v0 + c) * R.init_v;
+                if (SSD_INB(at, chains * K * V)) h = R.init[at] * R.init_scale;
+            }
+        }
+        sH[e] = h;
+    }
+    // a backward scan's initial state meets its first token undecayed
+    int off = (from_init && R.reverse) ? 0 : 1;
+    const int span = it.t1 - it.t0, nch = (span + kC - 1) / kC;
+    const float2 full = decay_power(la, kC);
+    const int cg = (tid & 15) * 4;  // 4 columns
+    const int rg = tid >> 4;        // 16 row groups
+
+    for (int c = 0; c < nch; ++c) {
+        const int ct = it.t0 + (R.reverse ? nch - 1 - c : c) * kC;
+        const int n = min(kC, it.t1 - ct);
+        __syncthreads();
+        if (kOut) load_rows<T>(R.q, it, ct, n, 0, K, L.K4, L.ldk, sQ, rows, batches);
+        load_rows<T>(R.k, it, ct, n, 0, K, L.K4, L.ldk, sK, rows, batches);
+        load_rows<T>(R.v, it, ct, n, v0, vn, kVT, kVT, sV, rows, batches);
+        __syncthreads();
+        if (kOut) {
+            // scores: row i, columns j0 + 8 m
+            const int i = tid >> 3, j0 = tid & 7;
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < L.K4; k += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(sQ + i * L.ldk + k);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float4 b = *reinterpret_cast<const float4*>(sK + (j0 + 8 * m) * L.ldk + k);
+                    s[m] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s[m]))));
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int j = j0 + 8 * m, d = R.reverse ? j - i : i - j;
+                sP[i * (kC + 4) + j] = (d >= 0 && i < n && j < n) ? s[m] * sTab[d] : 0.f;
+            }
+            __syncthreads();
+            // rows 2 rg, 2 rg + 1; columns cg .. cg + 3
+            float inter[2][4] = {}, intra[2][4] = {};
+            const int i0 = 2 * rg;
+            for (int k = 0; k < L.K4; k += 4) {
+                float qa[2][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    *reinterpret_cast<float4*>(qa[r]) = *reinterpret_cast<const float4*>(sQ + (i0 + r) * L.ldk + k);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const float4 h = *reinterpret_cast<const float4*>(sH + (k + kk) * kVT + cg);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        inter[r][0] = fmaf(qa[r][kk], h.x, inter[r][0]);
+                        inter[r][1] = fmaf(qa[r][kk], h.y, inter[r][1]);
+                        inter[r][2] = fmaf(qa[r][kk], h.z, inter[r][2]);
+                        inter[r][3] = fmaf(qa[r][kk], h.w, inter[r][3]);
+                    }
+                }
+            }
+            for (int j = 0; j < kC; j += 4) {
+                float pa[2][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    *reinterpret_cast<float4*>(pa[r]) =
+                        *reinterpret_cast<const float4*>(sP + (i0 + r) * (kC + 4) + j);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const float4 v = *reinterpret_cast<const float4*>(sV + (j + kk) * kVT + cg);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        intra[r][0] = fmaf(pa[r][kk], v.x, intra[r][0]);
+                        intra[r][1] = fmaf(pa[r][kk], v.y, intra[r][1]);
+                        intra[r][2] = fmaf(pa[r][kk], v.z, intra[r][2]);
+                        intra[r][3] = fmaf(pa[r][kk], v.w, intra[r][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int i1 = i0 + r;
+                if (i1 >= n) continue;
+                const float e = sTab[(R.reverse ? n - 1 - i1 : i1) + off];
+                const long long row = (long long)it.batch * rows + it.row0 + ct + i1;
+                const long long at = (row * H + it.head) * V + v0 + cg;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (cg + q >= vn || !SSD_INB(at + q, rows * batches * H * V)) continue;
+                    const float o = R.out_scale * fmaf(e, inter[r][q], intra[r][q]);
+                    if (R.out_f32) ((float*)R.out)[at + q] = o;
+                    else ((T*)R.out)[at + q] = from_f32<T>(o);
+                }
+            }
+            __syncthreads();  // every read of H before its update
+        }
+        const float2 dec = n - 1 + off == kC ? full : decay_power(la, n - 1 + off);
+        for (int e = tid; e < kC * L.K4; e += kThreads) {
+            const int j = e / L.K4, k = e - j * L.K4;
+            if (j < n) sK[j * L.ldk + k] *= sTab[R.reverse ? j : n - 1 - j];
+        }
+        __syncthreads();
+        for (int kb = 4 * rg; kb < L.K4; kb += 64) {
+            float acc[4][4] = {};
+#pragma unroll 4
+            for (int j = 0; j < kC; ++j) {
+                const float4 a = *reinterpret_cast<const float4*>(sK + j * L.ldk + kb);
+                const float4 b = *reinterpret_cast<const float4*>(sV + j * kVT + cg);
+                const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    acc[r][0] = fmaf(av[r], b.x, acc[r][0]);
+                    acc[r][1] = fmaf(av[r], b.y, acc[r][1]);
+                    acc[r][2] = fmaf(av[r], b.z, acc[r][2]);
+                    acc[r][3] = fmaf(av[r], b.w, acc[r][3]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float4* hp = reinterpret_cast<float4*>(sH + (kb + r) * kVT + cg);
+                float4 h = *hp;
+                h.x = fmaf(h.x, dec.x, fmaf(h.x, dec.y, acc[r][0]));
+                h.y = fmaf(h.y, dec.x, fmaf(h.y, dec.y, acc[r][1]));
+                h.z = fmaf(h.z, dec.x, fmaf(h.z, dec.y, acc[r][2]));
+                h.w = fmaf(h.w, dec.x, fmaf(h.w, dec.y, acc[r][3]));
+                *hp = h;
+            }
+        }
+        off = 1;
+    }
+    __syncthreads();
+    float* dst = nullptr;
+    float mul = 1.f;
+    if (!kOut) {
+        dst = p.states + it.slot * K * V;
+    } else if (R.fin && it.seg == it.nseg - 1) {
+        dst = R.fin + chain * K * V;
+        mul = R.fin_scale * (R.reverse && it.len > 0 ? decay_power(la, 1).x : 1.f);
+    }
+    if (dst) {
+        const long long extent = kOut ? chains * K * V : p.plan.slots() * K * V;
+        const float* dst0 = kOut ? R.fin : p.states;
+        (void)extent, (void)dst0;
+        for (int e = tid; e < K * kVT; e += kThreads) {
+            const int k = e / kVT, c = e % kVT;
+            if (c < vn && SSD_INB(dst - dst0 + (long long)k * V + v0 + c, extent)) dst[(long long)k * V + v0 + c] = sH[e] * mul;
+        }
+    }
+}
+
+// The state entering each item of a cut chain, in place: slot i holds what item
+// i builds from zero and becomes the state after it,
+//     e <- l^(tokens of item i) e + slot_i,
+// e starting as the chain's initial state.  `tiles` blocks per chain, a thread
+// per state element at a time; the work is one pass over the slots.
+__global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, int tiles) {
+    __shared__ ScanItem sItem;
+    const int HR = p.plan.H * p.plan.nroles;
+    const long long cr = blockIdx.x / tiles;  // chain and role
+    if (threadIdx.x < 32) {
+        ScanItem f;
+        f.valid = 0;
+        if (!p.plan.packed) {
+            f = scan_item(p.plan, p.plan.nfull + cr * p.plan.nseg);
+        } else {
+            // the first item of sequence cr / HR, behind the items of those before it
+            const int seq = (int)(cr / HR), lane = threadIdx.x;
+            const int begin = min(max(p.plan.cu[seq], 0), p.plan.T);
+            if (min(p.plan.cu[seq + 1], p.plan.T) - begin > p.plan.seg_tokens) {
+                long long before = 0;
+                for (int base = 0; base < seq; base += 32) {
+                    const int s = base + lane;
+                    int n = 0;
+                    if (s < seq) {
+                        const int c0 = min(max(p.plan.cu[s], 0), p.plan.T);
+                        const int len = min(max(p.plan.cu[s + 1], c0), p.plan.T) - c0;
+                        n = max(1, (len + p.plan.seg_tokens - 1) / p.plan.seg_tokens);
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+                    before += n;
+                }
+                f = scan_item(p.plan, before * HR + cr % HR);
+            }
+        }
+        if (threadIdx.x == 0) sItem = f;
+    }
+    __syncthreads();
+    const ScanItem it = sItem;
+    if (!it.valid || it.nseg < 2) return;
+    const ScanRole& R = p.role[it.role];
+    const int K = R.K, V = R.V;
+    const float la = p.decay[it.head];
+    const long long step = p.plan.packed ? HR : 1;
+    const long long chain = (long long)it.seq * p.plan.H + it.head;
+    const float2 whole = decay_power(la, p.plan.seg_tokens);
+    // the first item of a backward scan is the sequence's last, shorter piece,
+    // and its initial state meets the last token undecayed
+    const int n0 = R.reverse ? it.len - (it.nseg - 1) * p.plan.seg_tokens - 1 : p.plan.seg_tokens;
+    const float2 first = decay_power(la, n0);
+    for (int e = (blockIdx.x % tiles) * 256 + threadIdx.x; e < K * V; e += tiles * 256) {
+        float h = 0.f;
+        if (R.init) {
+            const long long at = chain * K * V + (e / V) * R.init_k + (e % V) * R.init_v;
+            if (SSD_INB(at, (long long)p.plan.B * p.plan.H * K * V)) h = R.init[at] * R.init_scale;
+        }
+        for (int i = 0; i + 1 < it.nseg; ++i) {
+            const long long slot = it.slot + i * step;
+            if (slot >= p.plan.slots()) break;  // decreasing offsets: the items behind do not run
+            const long long at = slot * K * V + e;
+            if (!SSD_INB(at, p.plan.slots() * K * V)) break;
+            const float2 d = i == 0 ? first : whole;
+            h = fmaf(h, d.x, fmaf(h, d.y, p.states[at]));
+            p.states[at] = h;
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) group_sum_kernel(const float* __restrict__ part, T* __restrict__ out,
+                                                        long long total, int D, int G, int share) {
+    for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < total; e += (long long)gridDim.x * 256) {
+        const int d = (int)(e % D);
+        const long long rg = e / D;  // row * G + g
+        const float* src = part + rg * share * D + d;
+        float s = 0.f;
+        for (int h = 0; h < share; ++h)
+            if (SSD_INB(rg * share * D + d + (long long)h * D, total * share)) s += src[(long long)h * D];
+        if (SSD_INB(e, total)) out[e] = from_f32<T>(s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_scan_simt(const ScanLaunch& s, bool state_only, cudaStream_t st) {
+    int V = 1, K = 1;
+    for (int r = 0; r < s.plan.nroles; ++r) {
+        V = s.role[r].V > V ? s.role[r].V : V;
+        K = s.role[r].K > K ? s.role[r].K : K;
+    }
+    const int ntiles = (V + kVT - 1) / kVT;
+    const long long grid = s.plan.items * ntiles;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const size_t smem = simt_layout(K).bytes;
+    auto kernel = s.bf16 ? (state_only ? scan_simt_kernel<__nv_bfloat16, false> : scan_simt_kernel<__nv_bfloat16, true>)
+                         : (state_only ? scan_simt_kernel<float, false> : scan_simt_kernel<float, true>);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)grid, kThreads, smem, st>>>(s, ntiles);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_scan_combine(const ScanLaunch& s, cudaStream_t st) {
+    int KV = 1;
+    for (int r = 0; r < s.plan.nroles; ++r) KV = s.role[r].K * s.role[r].V > KV ? s.role[r].K * s.role[r].V : KV;
+    // enough blocks to fill the GPU, none more: with many packed sequences most
+    // blocks find an uncut chain and leave
+    const long long all = (long long)s.plan.B * s.plan.H * s.plan.nroles;
+    const long long chains = s.plan.packed ? all : all - s.plan.nfull;
+    int tiles = (KV + 255) / 256;
+    while (tiles > 1 && chains * tiles > 148 * 16) tiles = (tiles + 1) / 2;
+    const long long grid = chains * tiles;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    scan_combine_kernel<<<(unsigned)grid, 256, 0, st>>>(s, tiles);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_group_sum(const float* part, void* out, long long rows, int H, int G, int D, bool bf16,
+                             cudaStream_t st) {
+    const long long total = rows * G * D;
+    const long long want = (total + 255) / 256;
+    const unsigned grid = (unsigned)(want < 148 * 16 ? want : 148 * 16);
+    if (bf16)
+        group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(part, (__nv_bfloat16*)out, total, D, G, H / G);
+    else
+        group_sum_kernel<float><<<grid, 256, 0, st>>>(part, (float*)out, total, D, G, H / G);
+    return cudaGetLastError();
+}
+
+}  // namespace ssd

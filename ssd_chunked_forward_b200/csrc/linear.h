@@ -1,0 +1,242 @@
+// linear.h -- what the linear-attention kernels share: the scan's operands,
+// how a launch is cut into items, and the launchers (internal; the public ABI
+// is include/ssd.h).
+//
+// Everything here is one scan.  With l = exp(decay[h]) and a state h[K][V],
+//     h_t = l h_{t-1} + k_t v_t^T,     out_t = out_scale * q_t^T h_t
+// the forward is that scan of (q, k, v), and each gradient is the same scan
+// with the roles of the tensors exchanged, backwards in time for dk and dv:
+//     dq: (dy, v, k) forwards     dk: (v, dy, q) backwards     dv: (k, q, dy) backwards
+// so one kernel serves them all, given a ScanRole for each.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define SSD_HD __host__ __device__
+#else
+#define SSD_HD
+#endif
+
+namespace ssd {
+
+// one tensor of rows [batch][token][head][d], strides in elements (d is contiguous)
+struct RowTensor {
+    const void* p;
+    long long batch, token, head;
+    int share;  // head h of the scan reads head h / share of the tensor
+};
+
+struct ScanRole {
+    RowTensor q, k, v;
+    int K, V;          // contraction and value sizes of this scan's state
+    int reverse;       // 1: from the last token to the first
+    float out_scale;
+    void* out;         // contiguous [rows][H][V], or null with a state-only scan
+    int out_f32;       // out holds fp32 whatever the inputs' type
+    // state of each chain before its first token, times init_scale; element
+    // (k, v) of chain c at init[c * K * V + k * init_k + v * init_v]; null = zero.
+    // A backward scan's initial state is added at the last token undecayed.
+    const float* init;
+    long long init_k, init_v;
+    float init_scale;
+    // state after the chain's last token times fin_scale (a backward scan: times
+    // the decay of one further token), [chain][K][V]; null = not wanted
+    float* fin;
+    float fin_scale;
+};
+
+constexpr int kScanRoles = 3;
+constexpr int kScanChunk = 128;  // segment bounds are multiples of this many tokens
+
+// How the chains (sequence, head, role) are cut into items, one per block.
+// Rows of equal length ([B][T]): the first `nfull` chains are one item each,
+// the others `nseg` items of seg_tokens tokens.  Packed rows: every sequence
+// is cut every seg_tokens tokens, and the items are counted on the device.
+// A chain of several items first has the state of each item but its last
+// built from zero (state-only items), then those states combined into the
+// state entering each item.
+struct ScanPlan {
+    int B, T, H, nroles;
+    int packed;
+    const int* cu;      // packed: [B+1] row offsets of the sequences
+    int nfull, nseg;
+    int seg_tokens;
+    long long items;    // upper bound when packed
+    // whether any chain can have several items
+    SSD_HD bool cut() const { return packed ? T > seg_tokens : nseg > 1; }
+    SSD_HD long long slots() const { return !cut() ? 0 : packed ? items : items - nfull; }
+};
+
+struct ScanLaunch {
+    ScanPlan plan;
+    ScanRole role[kScanRoles];
+    const float* decay;  // [H]
+    float* states;       // [slots][K][V] of the items that are not their chain's last
+    int* status;         // device status word
+    int reset;           // the call's first kernel: its first block clears the status word
+    bool bf16;
+};
+
+// The item `it` of a plan.
+struct ScanItem {
+    int role, seq, head;
+    int seg, nseg;          // position among the chain's items, in scan order
+    long long row0;         // first row of the sequence in the row dimension (0 when not packed)
+    int batch;              // batch coordinate (0 when packed)
+    int len;                // tokens of the sequence
+    int t0, t1;             // this item's tokens [t0, t1) of the sequence
+    long long slot, slot_prev;  // states: own, and the one this item starts from (-1: the chain's initial state)
+    int valid;
+};
+
+#ifdef __CUDACC__
+// Called by the 32 lanes of one warp; the result is the same in every lane.
+// Offsets that are no offsets (negative, beyond T, decreasing) are clamped, so
+// that no row outside [0, T) is ever addressed.
+__device__ inline ScanItem scan_item(const ScanPlan& p, long long it) {
+    ScanItem r;
+    r.valid = 0;
+    r.row0 = 0;
+    if (!p.packed) {
+        long long cr = it;
+        int seg = 0, nseg = 1;
+        r.slot = -1;
+        if (it >= p.nfull) {
+            const long long rest = it - p.nfull;
+            cr = p.nfull + rest / p.nseg;
+            seg = (int)(rest % p.nseg);
+            nseg = p.nseg;
+            r.slot = rest;
+        }
+        if (it >= p.items) return r;
+        r.role = (int)(cr % p.nroles);
+        cr /= p.nroles;
+        r.head = (int)(cr % p.H);
+        r.seq = (int)(cr / p.H);
+        r.batch = r.seq;
+        r.len = p.T;
+        r.seg = seg;
+        r.nseg = nseg;
+        r.slot_prev = seg > 0 ? r.slot - 1 : -1;
+        r.valid = 1;
+    } else {
+        const int lane = threadIdx.x & 31;
+        const int HR = p.H * p.nroles;
+        const long long unit = it / HR;
+        const int hr = (int)(it % HR);
+        r.role = hr % p.nroles;
+        r.head = hr / p.nroles;
+        r.batch = 0;
+        long long before = 0;
+        int found = 0;
+        for (int base = 0; base < p.B && !found; base += 32) {
+            const int s = base + lane;
+            int c0 = 0, len = 0, n = 0;
+            if (s < p.B) {
+                c0 = min(max(p.cu[s], 0), p.T);
+                len = min(max(p.cu[s + 1], c0), p.T) - c0;
+                n = max(1, (len + p.seg_tokens - 1) / p.seg_tokens);
+            }
+            int sum = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += u;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, before + sum > unit);
+            if (hit) {
+                const int w = __ffs(hit) - 1;
+                r.seq = base + w;
+                r.row0 = __shfl_sync(0xffffffffu, c0, w);
+                r.len = __shfl_sync(0xffffffffu, len, w);
+                r.nseg = __shfl_sync(0xffffffffu, n, w);
+                r.seg = (int)(unit - before) - (__shfl_sync(0xffffffffu, sum, w) - r.nseg);
+                found = 1;
+            } else {
+                before += __shfl_sync(0xffffffffu, sum, 31);
+            }
+        }
+        // offsets that decrease can ask for more items than there are slots for
+        if (!found || it >= p.items) return r;
+        r.slot = it;
+        r.slot_prev = r.seg > 0 ? it - HR : -1;
+        r.valid = 1;
+    }
+    return r;
+}
+// The tokens of the item, given the direction of its role.
+__device__ inline void scan_item_tokens(ScanItem& r, int seg_tokens, int reverse) {
+    if (r.nseg == 1) {
+        r.t0 = 0;
+        r.t1 = r.len;
+    } else {
+        const int j = reverse ? r.nseg - 1 - r.seg : r.seg;
+        r.t0 = j * seg_tokens;
+        r.t1 = min(r.len, r.t0 + seg_tokens);
+    }
+}
+// exp(decay * n) as an unevaluated sum of two fp32 numbers: a long chain
+// multiplies its state by the same factor at every chunk, and the error of one
+// rounded factor would grow with the number of chunks the state remembers.
+__device__ inline float2 decay_power(float decay, int n) {
+    const double e = n == 0 ? 1.0 : exp((double)decay * n);
+    const float hi = (float)e;
+    return make_float2(hi, (float)(e - (double)hi));
+}
+#endif
+
+// ---- launchers --------------------------------------------------------------
+// CUDA cores, fp32 arithmetic: any sizes up to 256, any strides.  state_only:
+// the states of the items that are not their chain's last, into `states`.
+cudaError_t launch_scan_simt(const ScanLaunch& s, bool state_only, cudaStream_t st);
+// Tensor cores (linear_tc.cu): bf16, sizes up to 128 and multiples of 8, rows
+// on 16-byte boundaries.
+bool scan_tc_supported(const ScanRole& r, const ScanPlan& p, bool bf16);
+cudaError_t launch_scan_tc(const ScanLaunch& s, bool state_only, cudaStream_t st);
+// states in place: slot i from "built by item i from zero" to "after item i"
+cudaError_t launch_scan_combine(const ScanLaunch& s, cudaStream_t st);
+// out[row][g][d] = sum over the heads of group g of part[row][h][d]
+cudaError_t launch_group_sum(const float* part, void* out, long long rows, int H, int G, int D, bool bf16,
+                             cudaStream_t st);
+
+struct LinearStep {
+    RowTensor q, k, v;
+    int B, H, K, V;
+    const float* decay;
+    float scale;
+    float* state;  // [B][H][K][V]
+    void* y;       // [B][H][V]
+    bool bf16;
+};
+cudaError_t launch_linear_step(const LinearStep& s, cudaStream_t st);
+
+struct NormArgs {
+    long long rows;
+    int width, groups;
+    bool bf16;
+    const void* x;
+    long long x_stride;
+    const float* weight;  // or null
+    const float* bias;    // or null
+    const void* gate;     // or null
+    long long gate_stride;
+    float eps;
+    void* y;
+    float* stats;  // [rows][groups][2], or null
+    // backward
+    const void* dy;
+    long long dy_stride;
+    void* dx;
+    float* dweight;  // or null
+    float* dbias;    // or null
+    void* dgate;
+    float* part;  // [norm_backward_parts][2][width]
+};
+cudaError_t launch_layer_norm(const NormArgs& a, cudaStream_t st);
+// rows of partial sums that the backward writes
+int norm_backward_parts(long long rows, int width, int groups, bool bf16);
+cudaError_t launch_layer_norm_backward(const NormArgs& a, cudaStream_t st);
+
+}  // namespace ssd

@@ -32,7 +32,9 @@ EXPORTS = [
     "ssd_segment_state", "ssd_backward", "ssd_backward_workspace_size",
     "ssd_test_fail_calls", "ssd_test_pending_failures", "ssd_split_pieces",
     "ssd_device_status_where", "ssd_forward_discretized", "ssd_debug_build", "ssd_debug_record",
-    "ssd_debug_fail_all",
+    "ssd_debug_fail_all", "ssd_linear_attention", "ssd_linear_workspace_size",
+    "ssd_linear_attention_step", "ssd_linear_attention_backward", "ssd_linear_backward_workspace_size",
+    "ssd_layer_norm", "ssd_layer_norm_backward", "ssd_layer_norm_backward_workspace_size",
 ]
 
 
@@ -47,6 +49,19 @@ class Shape(ctypes.Structure):
 
     def __repr__(self):
         return "Shape(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class LinearShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "H", "G", "K", "V", "dtype", "packed")]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_longlong) for n in ("batch", "token", "head")]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("width", ctypes.c_int), ("groups", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -108,6 +123,21 @@ def load(path: str = None):
     lib.ssd_backward.argtypes = [sp, vp, fp, vp, vp, fp, fp, vp, fp, vp, fp, vp, vp, fp, fp, vp, sz, vp]
     lib.ssd_backward_workspace_size.argtypes = [sp]
     lib.ssd_backward_workspace_size.restype = sz
+    lp, np_, stp, ll = ctypes.POINTER(LinearShape), ctypes.POINTER(NormShape), ctypes.POINTER(Strides), ctypes.c_longlong
+    qkv = [vp, stp, vp, stp, vp, stp]
+    lib.ssd_linear_attention.argtypes = [lp] + qkv + [fp, vp, fp, ctypes.c_float, vp, fp, vp, sz, vp]
+    lib.ssd_linear_attention_step.argtypes = [lp] + qkv + [fp, ctypes.c_float, fp, vp, vp]
+    lib.ssd_linear_attention_backward.argtypes = ([lp] + qkv + [fp, vp, fp, ctypes.c_float, vp, fp, vp, vp, vp, fp,
+                                                               vp, sz, vp])
+    lib.ssd_layer_norm.argtypes = [np_, vp, ll, fp, fp, vp, ll, ctypes.c_float, vp, fp, vp]
+    lib.ssd_layer_norm_backward.argtypes = [np_, vp, ll, fp, fp, vp, ll, vp, ll, fp, vp, fp, fp, vp, vp, sz, vp]
+    for name, arg in (("ssd_linear_workspace_size", lp), ("ssd_linear_backward_workspace_size", lp),
+                      ("ssd_layer_norm_backward_workspace_size", np_)):
+        getattr(lib, name).argtypes = [arg]
+        getattr(lib, name).restype = sz
+    for name in ("ssd_linear_attention", "ssd_linear_attention_step", "ssd_linear_attention_backward",
+                 "ssd_layer_norm", "ssd_layer_norm_backward"):
+        getattr(lib, name).restype = ctypes.c_int
     for name in ("ssd_forward_noalloc", "ssd_forward", "ssd_forward_path", "ssd_forward_init",
                  "ssd_device_status", "ssd_chunk_cumsum", "ssd_decode_step", "ssd_discretize",
                  "ssd_decay_total", "ssd_state_combine", "ssd_segment_state", "ssd_backward",
@@ -496,3 +526,257 @@ def backward(x, a, Bm, Cm, D, dy, chunk=256, *, dfinal=None, initial_state=None,
            "ssd_backward")
     return out
 
+
+# ---- linear attention with a decay for each head, and layer norm -------------
+#
+# These calls run on the device of their tensors, on its current torch stream
+# unless another is given.
+
+def _on_device(name, t, device, dtype=None, shape=None, contiguous=True):
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {str(dtype).replace('torch.', '')}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _dtype_code(t):
+    if t.dtype == torch.bfloat16:
+        return SSD_DTYPE_BF16
+    if t.dtype == torch.float32:
+        return SSD_DTYPE_F32
+    raise ValueError("tensors must be float32 or bfloat16")
+
+
+def _stream_of(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _stream(stream)
+
+
+def _linear_args(q, k, v, decay, cu_seqlens, step=False):
+    """The shape and the strides of q, k, v after their checks."""
+    lead = 1 if step or cu_seqlens is not None else 2
+    if q.dim() != lead + 2 or k.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError(f"q, k, v must have {lead + 2} dimensions")
+    dt = _dtype_code(q)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _on_device(name, t, q.device, q.dtype, contiguous=False)
+        if t.numel() == 0:
+            raise ValueError(f"{name} is empty")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+    rows, H, K = tuple(q.shape[:lead]), q.shape[-2], q.shape[-1]
+    G, V = k.shape[-2], v.shape[-1]
+    if tuple(k.shape) != rows + (G, K) or tuple(v.shape) != rows + (G, V) or H % G:
+        raise ValueError("k must be [..., G, K] and v [..., G, V] with q's leading dimensions and G dividing H")
+    _on_device("decay", decay, q.device, torch.float32, (H,))
+    if cu_seqlens is not None:
+        _on_device("cu_seqlens", cu_seqlens, q.device, torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be [sequences + 1]")
+        B, T, packed = cu_seqlens.numel() - 1, rows[0], 1
+    else:
+        B, T, packed = (rows[0], 1, 0) if step else (rows[0], rows[1], 0)
+    strides = []
+    for t in (q, k, v):
+        s = t.stride()
+        batch = 0 if packed else s[0]
+        strides.append(Strides(batch, 0 if step else s[lead - 1], s[-2]))
+    return LinearShape(B, T, H, G, K, V, dt, packed), strides, rows
+
+
+def _qkv(q, k, v, strides):
+    return [x for t, s in zip((q, k, v), strides) for x in (_ptr(t), ctypes.byref(s))]
+
+
+def _state_arg(name, t, shape, device):
+    if t is not None:
+        _on_device(name, t, device, torch.float32, (shape.B, shape.H, shape.K, shape.V))
+    return t
+
+
+def _workspace_arg(workspace, need, device, where):
+    if need == 0:
+        raise SSDError(SSD_ERR_INVALID_ARG, where)
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _on_device("workspace", workspace, device, torch.uint8)
+    return workspace
+
+
+def linear_workspace_size(shape: LinearShape) -> int:
+    return int(load().ssd_linear_workspace_size(ctypes.byref(shape)))
+
+
+def linear_backward_workspace_size(shape: LinearShape) -> int:
+    return int(load().ssd_linear_backward_workspace_size(ctypes.byref(shape)))
+
+
+def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqlens=None, y=None, final_state=None,
+                     want_final=True, workspace=None, stream=None):
+    """y and the final state of linear attention with a decay for each head:
+    h_t = exp(decay[h]) h_{t-1} + k_t v_t^T, y_t = scale q_t^T h_t.
+
+    q [B,T,H,K], k [B,T,G,K], v [B,T,G,V] (float32 or bfloat16; slices of one
+    projection are taken as they are, only the last dimension has to be
+    contiguous), decay [H] float32 log-decays, initial_state [B,H,K,V] float32
+    or None (zero), scale (None: K**-0.5).  With cu_seqlens (int32 [S+1], on the device) the
+    tensors are [T,heads,d] with S sequences one behind the other, the states
+    [S,H,K,V]; rows of a given y outside every sequence stay as they are.
+    Returns y [B,T,H,V] and the state [B,H,K,V] float32 (None with
+    want_final=False).  Asynchronous on the current stream of q's device."""
+    shape, strides, rows = _linear_args(q, k, v, decay, cu_seqlens)
+    dev = q.device
+    _state_arg("initial_state", initial_state, shape, dev)
+    if y is None:
+        y = torch.empty(rows + (shape.H, shape.V), dtype=q.dtype, device=dev)
+    _on_device("y", y, dev, q.dtype, rows + (shape.H, shape.V))
+    if final_state is None and want_final:
+        final_state = torch.empty((shape.B, shape.H, shape.K, shape.V), dtype=torch.float32, device=dev)
+    _state_arg("final_state", final_state, shape, dev)
+    workspace = _workspace_arg(workspace, linear_workspace_size(shape), dev, "ssd_linear_workspace_size")
+    with torch.cuda.device(dev):
+        _check(load().ssd_linear_attention(
+            ctypes.byref(shape), *_qkv(q, k, v, strides), _ptr(decay), _ptr(cu_seqlens), _ptr(initial_state),
+            float(shape.K ** -0.5 if scale is None else scale), _ptr(y), _ptr(final_state), _ptr(workspace),
+            workspace.numel(), _stream_of(stream, dev)), "ssd_linear_attention")
+    return y, final_state
+
+
+def linear_attention_step(q, k, v, decay, state, *, scale=None, y=None, stream=None):
+    """One token of linear_attention() for a batch of sequences, in place on
+    ``state`` [B,H,K,V] float32: q [B,H,K], k [B,G,K], v [B,G,V], decay [H].
+    Returns y [B,H,V]."""
+    shape, strides, rows = _linear_args(q, k, v, decay, None, step=True)
+    dev = q.device
+    _state_arg("state", state, shape, dev)
+    if y is None:
+        y = torch.empty(rows + (shape.H, shape.V), dtype=q.dtype, device=dev)
+    _on_device("y", y, dev, q.dtype, rows + (shape.H, shape.V))
+    with torch.cuda.device(dev):
+        _check(load().ssd_linear_attention_step(
+            ctypes.byref(shape), *_qkv(q, k, v, strides), _ptr(decay),
+            float(shape.K ** -0.5 if scale is None else scale), _ptr(state), _ptr(y), _stream_of(stream, dev)),
+            "ssd_linear_attention_step")
+    return y
+
+
+def linear_attention_backward(q, k, v, decay, dy, *, scale=None, initial_state=None, dfinal=None, cu_seqlens=None,
+                              want_dinit=True, workspace=None, stream=None):
+    """Gradients of sum(dy * y) + <dfinal, final_state> of linear_attention()
+    for the same inputs: a dict of dq, dk, dv (contiguous, in q's dtype; dk and
+    dv summed over the query heads of their group) and dinit ([B,H,K,V]
+    float32, or None).  dy like y; dfinal like the final state, or None.  The
+    decay has no gradient.  Rows outside every packed sequence come back zero."""
+    shape, strides, rows = _linear_args(q, k, v, decay, cu_seqlens)
+    dev = q.device
+    _on_device("dy", dy, dev, q.dtype, rows + (shape.H, shape.V))
+    _state_arg("initial_state", initial_state, shape, dev)
+    _state_arg("dfinal", dfinal, shape, dev)
+    new = torch.empty if cu_seqlens is None else torch.zeros
+    out = {
+        "dq": new(rows + (shape.H, shape.K), dtype=q.dtype, device=dev),
+        "dk": new(rows + (shape.G, shape.K), dtype=q.dtype, device=dev),
+        "dv": new(rows + (shape.G, shape.V), dtype=q.dtype, device=dev),
+        "dinit": (torch.empty((shape.B, shape.H, shape.K, shape.V), dtype=torch.float32, device=dev)
+                  if want_dinit else None),
+    }
+    workspace = _workspace_arg(workspace, linear_backward_workspace_size(shape), dev,
+                               "ssd_linear_backward_workspace_size")
+    with torch.cuda.device(dev):
+        _check(load().ssd_linear_attention_backward(
+            ctypes.byref(shape), *_qkv(q, k, v, strides), _ptr(decay), _ptr(cu_seqlens), _ptr(initial_state),
+            float(shape.K ** -0.5 if scale is None else scale), _ptr(dy), _ptr(dfinal), _ptr(out["dq"]),
+            _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dinit"]), _ptr(workspace), workspace.numel(),
+            _stream_of(stream, dev)), "ssd_linear_attention_backward")
+    return out
+
+
+def _norm_rows(name, t, like=None):
+    """t as rows: (row stride in elements); its leading dimensions must be one."""
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"{name} must have x's shape and dtype")
+    if t.dim() == 0 or t.numel() == 0:
+        raise ValueError(f"{name} is empty")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    stride = None  # of the flattened rows
+    want = None
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if want is None:
+            stride = s
+        elif s != want:
+            raise ValueError(f"the leading dimensions of {name} must flatten to rows")
+        want = s * n
+    return t.shape[-1] if stride is None else stride
+
+
+def _norm_args(x, weight, bias, groups, gate):
+    _on_device("x", x, x.device, contiguous=False)
+    x_stride = _norm_rows("x", x)
+    width = x.shape[-1]
+    if int(groups) < 1 or width % int(groups):
+        raise ValueError("groups must divide x's last dimension")
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _on_device(name, t, x.device, torch.float32, (width,))
+    gate_stride = 0
+    if gate is not None:
+        _on_device("gate", gate, x.device, contiguous=False)
+        gate_stride = _norm_rows("gate", gate, x)
+    return NormShape(x.numel() // width, width, int(groups), _dtype_code(x)), x_stride, gate_stride
+
+
+def layer_norm(x, weight=None, bias=None, *, groups=1, gate=None, eps=1e-5, y=None, stream=None):
+    """Layer norm over each of the ``groups`` equal parts of x's last dimension
+    (groups = heads: the norm behind a sequence mixer), times silu(gate):
+    y = ((x - mean) rstd weight + bias) silu(gate).
+
+    x [..., D] float32 or bfloat16 (leading dimensions that flatten to rows,
+    the last contiguous), gate the same or None, weight and bias [D] float32 or
+    None.  Returns y and stats [rows, groups, 2] float32 (mean and rstd, for
+    layer_norm_backward)."""
+    shape, xs, gs = _norm_args(x, weight, bias, groups, gate)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _on_device("y", y, x.device, x.dtype, x.shape)
+    stats = torch.empty((shape.rows, shape.groups, 2), dtype=torch.float32, device=x.device)
+    with torch.cuda.device(x.device):
+        _check(load().ssd_layer_norm(ctypes.byref(shape), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(gate), gs,
+                                     float(eps), _ptr(y), _ptr(stats), _stream_of(stream, x.device)),
+               "ssd_layer_norm")
+    return y, stats
+
+
+def layer_norm_backward(x, weight, bias, dy, stats, *, groups=1, gate=None, want_dweight=True, want_dbias=True,
+                        workspace=None, stream=None):
+    """Gradients of sum(dy * y) of layer_norm() for the same inputs and its
+    stats: a dict of dx, dgate (None without a gate), dweight and dbias ([D]
+    float32, or None)."""
+    shape, xs, gs = _norm_args(x, weight, bias, groups, gate)
+    dev = x.device
+    _on_device("dy", dy, dev, contiguous=False)
+    ds = _norm_rows("dy", dy, x)
+    _on_device("stats", stats, dev, torch.float32, (shape.rows, shape.groups, 2))
+    new = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device=dev)  # noqa: E731
+    out = {
+        "dx": new(*x.shape, dtype=x.dtype),
+        "dgate": new(*x.shape, dtype=x.dtype) if gate is not None else None,
+        "dweight": new(shape.width) if want_dweight else None,
+        "dbias": new(shape.width) if want_dbias else None,
+    }
+    if want_dweight or want_dbias:
+        workspace = _workspace_arg(workspace, int(load().ssd_layer_norm_backward_workspace_size(ctypes.byref(shape))),
+                                   dev, "ssd_layer_norm_backward_workspace_size")
+    with torch.cuda.device(dev):
+        _check(load().ssd_layer_norm_backward(
+            ctypes.byref(shape), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(gate), gs, _ptr(dy), ds, _ptr(stats),
+            _ptr(out["dx"]), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dgate"]), _ptr(workspace),
+            workspace.numel() if workspace is not None else 0, _stream_of(stream, dev)), "ssd_layer_norm_backward")
+    return out

@@ -1,0 +1,331 @@
+"""Linear attention with a decay for each head on the GPU, against the
+recurrence in 64 bits: prompts, gradients, single tokens, and their runs
+together."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests.linear_cases import bounds, heads64, on_tensor_cores, reference, slopes
+from ssd_chunked_forward_b200 import ssd
+from ssd_chunked_forward_b200.autograd import layer_norm_autograd, linear_attention_autograd
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def make(dtype, cuts, total, H, G, K, V, seed=1, init=True, fused=False, outside=None):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s, dt=dtype: torch.randn(s, generator=g, device="cuda").to(dt)  # noqa: E731
+    S = len(cuts) - 1
+    if fused:
+        q, k, v = rnd(total, H * K + G * (K + V)).split([H * K, G * K, G * V], -1)
+        q, k, v = q.unflatten(-1, (H, K)), k.unflatten(-1, (G, K)), v.unflatten(-1, (G, V))
+    else:
+        q, k, v = rnd(total, H, K), rnd(total, G, K), rnd(total, G, V)
+    out = {"q": q, "k": k, "v": v, "dy": rnd(total, H, V), "decay": slopes(H),
+           "init": rnd(S, H, K, V, dt=F32) if init else None, "dfinal": rnd(S, H, K, V, dt=F32) if init else None}
+    if outside is not None:  # rows of no sequence
+        dead = torch.ones(total, dtype=torch.bool, device="cuda")
+        for a, b in zip(cuts, cuts[1:]):
+            dead[a:b] = False
+        for n in ("q", "k", "v", "dy"):
+            out[n][dead] = outside
+    return out
+
+
+def check(got, ref, size, dtype, K, V, longest, tc):
+    for name, t in got.items():
+        if t is None:
+            continue
+        live = ~torch.isnan(ref[name])
+        d = (t.double() - ref[name]).abs()
+        b = bounds(ref, size, name, dtype, K, V, longest, tc)
+        bad = (d > b) | torch.isnan(d)
+        assert not bool((bad & live).any()), f"{name}: {int((bad & live).sum())} of {live.sum()} off, worst {float((d / b)[live].max()):.2f} of its bound"
+
+
+def both(c, cuts, dtype, scale=None, tc=None):
+    """Runs the forward and the backward as packed rows and checks every output."""
+    K, V = c["q"].shape[-1], c["v"].shape[-1]
+    longest = max(b - a for a, b in zip(cuts, cuts[1:]))
+    tc = on_tensor_cores(dtype, K, V) if tc is None else tc
+    sc = K ** -0.5 if scale is None else scale
+    args = (c["q"], c["k"], c["v"], c["decay"], sc, c["init"], cuts, c["dy"], c["dfinal"])
+    ref, size = reference(*args), reference(*args, magnitude=True)
+    cu = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    y, final = ssd.linear_attention(c["q"], c["k"], c["v"], c["decay"], scale=scale, initial_state=c["init"],
+                                    cu_seqlens=cu)
+    g = ssd.linear_attention_backward(c["q"], c["k"], c["v"], c["decay"], c["dy"], scale=scale,
+                                      initial_state=c["init"], dfinal=c["dfinal"], cu_seqlens=cu)
+    check({"y": y, "final": final, **g}, ref, size, dtype, K, V, longest, tc)
+    return y, final, g
+
+
+DIMS = [(64, 64), (128, 64), (64, 128), (128, 128), (96, 80), (16, 48), (8, 8), (100, 36), (1, 1), (33, 7)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("K,V", DIMS)
+@pytest.mark.parametrize("T", [1, 2, 33, 128, 129, 300])
+def test_rows_of_one_length(dtype, K, V, T):
+    """[B,T] rows: forward and gradients, shared heads, states in and out."""
+    B, H, G = 2, 4, 2
+    c = make(dtype, [0, T, 2 * T], B * T, H, G, K, V)
+    args = (c["q"], c["k"], c["v"], c["decay"], K ** -0.5, c["init"], [0, T, 2 * T], c["dy"], c["dfinal"])
+    ref, size = reference(*args), reference(*args, magnitude=True)
+    r = lambda t: t.view(B, T, *t.shape[1:])  # noqa: E731
+    y, final = ssd.linear_attention(r(c["q"]), r(c["k"]), r(c["v"]), c["decay"], initial_state=c["init"])
+    g = ssd.linear_attention_backward(r(c["q"]), r(c["k"]), r(c["v"]), c["decay"], r(c["dy"]),
+                                      initial_state=c["init"], dfinal=c["dfinal"])
+    got = {n: t.flatten(0, 1) if n not in ("final", "dinit") else t for n, t in {"y": y, "final": final, **g}.items()}
+    check(got, ref, size, dtype, K, V, T, on_tensor_cores(dtype, K, V))
+
+
+@pytest.mark.parametrize("K,V", [(256, 256), (200, 136), (128, 256)])
+def test_wide_heads(K, V):
+    for dtype in (F32, BF):
+        both(make(dtype, [0, 150], 150, 2, 1, K, V), [0, 150], dtype)
+
+
+PACKED = [[0, 5], [0, 0, 7, 7, 135, 300, 300], [0, 128, 256, 257, 700], [3, 60, 260]]
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF, 128, 128), (BF, 128, 64), (BF, 64, 64), (BF, 40, 112), (F32, 48, 64)])
+@pytest.mark.parametrize("cuts", PACKED, ids=str)
+def test_packed(dtype, K, V, cuts):
+    """Empty sequences, one token, ends inside a chunk; rows behind and before
+    the sequences hold NaN: they are not read, and a given y keeps its own."""
+    total = cuts[-1] + 37
+    c = make(dtype, cuts, total, 4, 4, K, V, outside=float("nan"), fused=True)
+    both(c, cuts, dtype)
+    y = torch.full((total, 4, V), 7.0, dtype=dtype, device="cuda")
+    ssd.linear_attention(c["q"], c["k"], c["v"], c["decay"], y=y, want_final=False,
+                         cu_seqlens=torch.tensor(cuts, dtype=torch.int32, device="cuda"))
+    assert bool((y[cuts[-1]:] == 7.0).all()) and bool((y[:cuts[0]] == 7.0).all())
+    assert bool(torch.isfinite(y[cuts[0]:cuts[-1]]).all())
+
+
+@pytest.mark.parametrize("dtype,K,V,T", [(BF, 128, 64, 3000), (BF, 128, 128, 2049), (BF, 64, 64, 5000),
+                                         (BF, 64, 128, 2500), (F32, 64, 32, 2000)])
+def test_long_cut_chains(dtype, K, V, T):
+    """Few chains: every chain is cut into items and its states combined; rows
+    of one length and packed ones give the same sums in other orders."""
+    c = make(dtype, [0, T], T, 2, 1, K, V)
+    y, final, g = both(c, [0, T], dtype)
+    e = lambda t: t[None]  # noqa: E731
+    args = (c["q"], c["k"], c["v"], c["decay"], K ** -0.5, c["init"], [0, T], c["dy"], c["dfinal"])
+    ref, size = reference(*args), reference(*args, magnitude=True)
+    y2, f2 = ssd.linear_attention(e(c["q"]), e(c["k"]), e(c["v"]), c["decay"], initial_state=c["init"])
+    g2 = ssd.linear_attention_backward(e(c["q"]), e(c["k"]), e(c["v"]), c["decay"], e(c["dy"]),
+                                       initial_state=c["init"], dfinal=c["dfinal"])
+    got = {"y": y2[0], "final": f2, "dq": g2["dq"][0], "dk": g2["dk"][0], "dv": g2["dv"][0], "dinit": g2["dinit"]}
+    check(got, ref, size, dtype, K, V, T, on_tensor_cores(dtype, K, V))
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF, 128, 64), (BF, 64, 128), (F32, 20, 24)])
+def test_some_chains_cut(dtype, K, V):
+    """More chains than run at a time: whole ones, then cut ones."""
+    B, T, H = 3, 1100, 52
+    c = make(dtype, [0, T, 2 * T, 3 * T], B * T, H, H, K, V, init=False)
+    args = (c["q"], c["k"], c["v"], c["decay"], K ** -0.5, None, [0, T, 2 * T, 3 * T])
+    ref, size = reference(*args), reference(*args, magnitude=True)
+    r = lambda t: t.view(B, T, *t.shape[1:])  # noqa: E731
+    y, final = ssd.linear_attention(r(c["q"]), r(c["k"]), r(c["v"]), c["decay"])
+    check({"y": y.flatten(0, 1), "final": final}, ref, size, dtype, K, V, T, on_tensor_cores(dtype, K, V))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_decays_at_the_ends(dtype):
+    """No decay, decays that leave one token, and a head that keeps nothing."""
+    c = make(dtype, [0, 290], 290, 4, 4, 64, 64)
+    c["decay"] = torch.tensor([0.0, -3.0, -90.0, float("-inf")], device="cuda")
+    both(c, [0, 290], dtype)
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF, 128, 64), (BF, 72, 40), (F32, 64, 64), (BF, 50, 30)])
+def test_strides(dtype, K, V):
+    """Batch of slices of one projection, heads before tokens, a broadcast batch,
+    and rows that start off a 16-byte boundary."""
+    B, T, H, G = 2, 200, 4, 2
+    cuts = [0, T, 2 * T]
+    c = make(dtype, cuts, B * T, H, G, K, V)
+    args = (c["q"], c["k"], c["v"], c["decay"], K ** -0.5, c["init"], cuts, c["dy"], c["dfinal"])
+    ref, size = reference(*args), reference(*args, magnitude=True)
+    rows = {n: c[n].view(B, T, *c[n].shape[1:]) for n in ("q", "k", "v", "dy")}
+
+    def wide(t, left):  # a slice of a wider projection
+        b = torch.full(t.shape[:2] + (left + t.shape[2] * t.shape[3] + 24,), float("nan"), dtype=dtype, device="cuda")
+        s = b[..., left:left + t.shape[2] * t.shape[3]].unflatten(-1, t.shape[2:])
+        s.copy_(t)
+        return s
+
+    forms = {"slices": lambda t: wide(t, 8), "odd start": lambda t: wide(t, 3),
+             "heads first": lambda t: t.transpose(1, 2).contiguous().transpose(1, 2)}
+    for name, form in forms.items():
+        q, k, v = (form(rows[n]) for n in "qkv")
+        y, final = ssd.linear_attention(q, k, v, c["decay"], initial_state=c["init"])
+        g = ssd.linear_attention_backward(q, k, v, c["decay"], rows["dy"], initial_state=c["init"], dfinal=c["dfinal"])
+        got = {n: t.flatten(0, 1) if n not in ("final", "dinit") else t for n, t in {"y": y, "final": final, **g}.items()}
+        check(got, ref, size, dtype, K, V, T, on_tensor_cores(dtype, K, V))
+    one = rows["k"][:1].expand(B, -1, -1, -1)
+    y, _ = ssd.linear_attention(rows["q"], one, rows["v"], c["decay"])
+    y2, _ = ssd.linear_attention(rows["q"], one.contiguous(), rows["v"], c["decay"])
+    longest = (y.double() - y2.double()).abs().max()
+    assert longest <= 4 * 2 ** -8 * y2.double().abs().max()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,H,G,K,V", [(1, 1, 1, 1, 1), (3, 4, 2, 128, 64), (2, 6, 1, 64, 128), (5, 2, 2, 128, 128),
+                                       (2, 2, 2, 256, 256), (2, 4, 4, 100, 36), (3, 2, 1, 33, 7), (1, 2, 2, 17, 130)])
+def test_step(dtype, B, H, G, K, V):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    q, k, v = rnd(B, H * K + G * (K + V) + 5).to(dtype)[:, 5:].split([H * K, G * K, G * V], -1)
+    q, k, v = q.unflatten(-1, (H, K)), k.unflatten(-1, (G, K)), v.unflatten(-1, (G, V))
+    state, decay = rnd(B, H, K, V), slopes(H)
+    lam = torch.exp(decay.double())[:, None, None]
+    kv = heads64(k, H)[..., None] * heads64(v, H)[..., None, :]
+    h = lam * state.double() + kv
+    y = 0.7 * torch.einsum("bhk,bhkv->bhv", q.double(), h)
+    size_h = lam * state.double().abs() + kv.abs()
+    size = 0.7 * torch.einsum("bhk,bhkv->bhv", q.double().abs(), size_h)
+    got = ssd.linear_attention_step(q, k, v, decay, state, scale=0.7)
+    # state: product, factor and sum round once each; y: K additions more
+    assert bool(((state.double() - h).abs() <= 4 * 2 ** -24 * size_h).all())
+    b = size * (K + 8) * 2 ** -24 + (2 ** -8 * 1.01 * y.abs() + size * 2 ** -20 if dtype == BF else 0.0)
+    assert bool(((got.double() - y).abs() <= b).all())
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF, 128, 64), (F32, 64, 64), (BF, 128, 128)])
+def test_prompt_then_tokens(dtype, K, V):
+    """A prompt in two calls and single tokens behind it are one sequence."""
+    T, n1, n2, B, H = 210, 130, 70, 2, 4
+    c = make(dtype, [0, T, 2 * T], B * T, H, 2, K, V, init=False)
+    args = (c["q"], c["k"], c["v"], c["decay"], K ** -0.5, None, [0, T, 2 * T])
+    ref, size = reference(*args), reference(*args, magnitude=True)
+    q, k, v = (c[n].view(B, T, *c[n].shape[1:]) for n in "qkv")
+    y1, state = ssd.linear_attention(q[:, :n1], k[:, :n1], v[:, :n1], c["decay"])
+    # the state updated in place: final_state is initial_state
+    y2, state2 = ssd.linear_attention(q[:, n1:n1 + n2], k[:, n1:n1 + n2], v[:, n1:n1 + n2], c["decay"],
+                                      initial_state=state, final_state=state)
+    assert state2 is state
+    ys = [y1, y2]
+    for t in range(n1 + n2, T):
+        ys.append(ssd.linear_attention_step(q[:, t], k[:, t], v[:, t], c["decay"], state)[:, None])
+    y = torch.cat(ys, 1).flatten(0, 1)
+    check({"y": y, "final": state}, ref, size, dtype, K, V, T, on_tensor_cores(dtype, K, V))
+
+
+def test_streams_and_graphs():
+    """On another stream, and captured into a graph that replays with new inputs
+    (cut chains, so several kernels and the workspace are in it)."""
+    T = 2300
+    c = make(BF, [0, T], T, 2, 2, 128, 64)
+    e = lambda t: t[None]  # noqa: E731
+    call = lambda: (ssd.linear_attention(e(c["q"]), e(c["k"]), e(c["v"]), c["decay"], initial_state=c["init"]),  # noqa: E731
+                    ssd.linear_attention_backward(e(c["q"]), e(c["k"]), e(c["v"]), c["decay"], e(c["dy"]),
+                                                  initial_state=c["init"], dfinal=c["dfinal"]))
+    flat = lambda r: list(r[0]) + [r[1][n] for n in sorted(r[1])]  # noqa: E731
+    want = flat(call())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = flat(call())
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = flat(call())
+    graph.replay()
+    for a, b, d in zip(want, other, held):
+        assert torch.equal(a, b) and torch.equal(a, d)
+    c["q"].mul_(-1.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(held[0], -want[0])
+    # two streams at once, a workspace each
+    ws = [torch.empty(ssd.linear_workspace_size(ssd.LinearShape(1, T, 2, 2, 128, 64, ssd.SSD_DTYPE_BF16, 0)),
+                      dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ys = []
+    torch.cuda.synchronize()
+    for w in ws:
+        s = torch.cuda.Stream()
+        ys.append(ssd.linear_attention(e(c["q"]), e(c["k"]), e(c["v"]), c["decay"], initial_state=c["init"],
+                                       workspace=w, stream=s)[0])
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], held[0]) and torch.equal(ys[1], held[0])
+    assert ssd.device_status(ws[0]) == ssd.SSD_OK
+
+
+def test_autograd_block():
+    """A block as a model has it: projection, linear attention, norm over the
+    heads with a gate; gradients against float64 autograd and differences."""
+    B, T, H, G, D, W = 2, 70, 4, 2, 32, 48
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x, w = rnd(B, T, W), (rnd(W, H * D + 2 * G * D + H * D) / W ** 0.5).requires_grad_()
+    nw, nb = (1 + 0.1 * rnd(H * D)).requires_grad_(), (0.1 * rnd(H * D)).requires_grad_()
+    h0 = rnd(B, H, D, D).requires_grad_()
+    decay, out = slopes(H), rnd(B, T, H * D)
+
+    def block(w, nw, nb, h0, lib):
+        q, k, v, z = (x.to(w.dtype) @ w).split([H * D, G * D, G * D, H * D], -1)
+        q, k, v = q.unflatten(-1, (H, D)), k.unflatten(-1, (G, D)), v.unflatten(-1, (G, D))
+        if lib:
+            y, fin = linear_attention_autograd(q, k, v, decay, initial_state=h0)
+            y = layer_norm_autograd(y.flatten(2), nw, nb, groups=H, gate=z)
+        else:
+            k, v = k.repeat_interleave(H // G, 2), v.repeat_interleave(H // G, 2)
+            h, ys = h0, []
+            for t in range(T):
+                h = torch.exp(decay.double())[:, None, None] * h + k[:, t, :, :, None] * v[:, t, :, None]
+                ys.append(D ** -0.5 * torch.einsum("bhk,bhkv->bhv", q[:, t], h))
+            y, fin = torch.stack(ys, 1), h
+            y = (y - y.mean(-1, keepdim=True)) / torch.sqrt(y.var(-1, unbiased=False, keepdim=True) + 1e-5)
+            y = (y.flatten(2) * nw + nb) * z * torch.sigmoid(z)
+        return (y * out.to(y.dtype)).sum() + (fin * 0.1).sum()
+
+    loss = block(w, nw, nb, h0, True)
+    got = torch.autograd.grad(loss, [w, nw, nb, h0])
+    leaves = [t.detach().double().requires_grad_() for t in (w, nw, nb, h0)]
+    ref_loss = block(*leaves, False)
+    want = torch.autograd.grad(ref_loss, leaves)
+    # products over W, K, T and rows in fp32: some hundred roundings, the norm's
+    # division amplifies by rstd at most tenfold here
+    for a, b in zip(got, want):
+        assert float((a.double() - b).norm() / b.norm()) <= 4000 * 2 ** -24
+    # differences, in float64 on the definition and once through the kernels
+    d = [torch.randn_like(t) for t in leaves]
+    eps = 1e-5
+    hi = block(*[t + eps * u for t, u in zip(leaves, d)], False)
+    lo = block(*[t - eps * u for t, u in zip(leaves, d)], False)
+    slope = float((hi - lo) / (2 * eps))
+    along = float(sum((a.double() * u).sum() for a, u in zip(got, d)))
+    assert abs(slope - along) <= 1e-4 * sum(float(a.double().norm() * u.norm()) for a, u in zip(got, d))
+
+
+def test_backward_captured_while_an_eager_graph_lives():
+    """Gradients by the explicit call inside a capture, with an autograd graph of
+    the same tensors alive."""
+    c = make(BF, [0, 100], 100, 2, 2, 64, 64)
+    q = c["q"][None].detach().requires_grad_()
+    y, _ = linear_attention_autograd(q, c["k"][None], c["v"][None], c["decay"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g = ssd.linear_attention_backward(q.detach(), c["k"][None], c["v"][None], c["decay"], c["dy"][None])
+    graph.replay()
+    (eager,) = torch.autograd.grad(y, q, c["dy"][None])
+    assert torch.equal(eager, g["dq"])
+
+
+def test_offsets_that_are_none_stay_inside():
+    """Decreasing, negative and too large offsets: clamped, nothing outside the
+    rows is written."""
+    T = 700
+    c = make(BF, [0, T], T, 2, 2, 64, 64, init=False)
+    for cuts in ([0, 600, 100, 700], [-50, 300, 5000], [700, 0, 700]):
+        cu = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+        guard = torch.full((T + 256, 2, 64), 3.0, dtype=BF, device="cuda")
+        y, _ = ssd.linear_attention(c["q"], c["k"], c["v"], c["decay"], cu_seqlens=cu, y=guard[128:128 + T])
+        torch.cuda.synchronize()
+        assert bool((guard[:128] == 3.0).all()) and bool((guard[128 + T:] == 3.0).all())
