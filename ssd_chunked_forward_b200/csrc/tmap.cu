@@ -45,6 +45,31 @@ cudaError_t make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t d0, u
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_tmap_bf16_rows(CUtensorMap* map, const void* base, uint64_t d, uint64_t heads, uint64_t tokens,
+                                uint64_t batches, long long head_stride, long long token_stride,
+                                long long batch_stride, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    if (((uintptr_t)base & 15u) != 0 || d % 8 != 0) return cudaErrorInvalidValue;
+    const cuuint64_t dims[4] = {d, heads, tokens, batches};
+    const long long given[3] = {head_stride, token_stride, batch_stride};
+    cuuint64_t strides[3];
+    for (int i = 0; i < 3; ++i) {
+        if (dims[i + 1] == 1) {
+            strides[i] = d * 2;
+            continue;
+        }
+        if (given[i] <= 0 || given[i] % 8 != 0 || given[i] >= (1LL << 39)) return cudaErrorInvalidValue;
+        strides[i] = (cuuint64_t)given[i] * 2;
+    }
+    const cuuint32_t box[4] = {64, 1, box_rows, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_tmap_f32_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                              uint64_t d3, uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();

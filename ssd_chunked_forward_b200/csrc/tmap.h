@@ -18,6 +18,13 @@ namespace ssd {
 cudaError_t make_tmap_bf16_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1,
                               uint64_t d2, uint64_t d3, uint32_t box_rows);
 
+// The same box over rows [batches][tokens][heads][d] of any strides (in
+// elements; d is contiguous).  A dimension of size 1 may have any stride;
+// the others' must be positive multiples of 8 (16 bytes).
+cudaError_t make_tmap_bf16_rows(CUtensorMap* map, const void* base, uint64_t d, uint64_t heads, uint64_t tokens,
+                                uint64_t batches, long long head_stride, long long token_stride,
+                                long long batch_stride, uint32_t box_rows);
+
 // A 4-D fp32 tensor map over a row-major [d3][d2][d1][d0] array (d0 <= 256
 // innermost, e.g. the per-state log-decays [B][T][H][N]), box (d0, 1, rows,
 // 1) without swizzle: one box lands as `rows` dense rows of d0 floats.  Rows
