@@ -20,7 +20,7 @@
 // outputs.  l^n multiplies H at every chunk and is kept as a sum of two fp32
 // numbers, or its rounding would grow with the number of chunks.
 //
-// Warp roles (576 threads):
+// Warp roles (608 threads):
 //   0-3    scores -> P (thread = row i)
 //   4-7    w o K: the first piece in K's own place in shared memory once the
 //          scores are done, the others in two buffers of 32 tokens in turn;
@@ -28,6 +28,9 @@
 //          packed sequences they hold the next sequence's tokens)
 //   8-15   state and output (two warps per TMEM lane quadrant)
 //   16     TMA loads; 17  TMEM, MMA issue
+//   18     TMA stores: the output tile takes the place of the chunk's K in shared
+//          memory (plain stores of rows by their threads touch 32 lines each: they
+//          kept the load/store unit busy for 2000 of a chunk's cycles)
 // MMA order per chunk: S, Q H, half of Z, P V, the other half of Z, so that the
 // next chunk's S finds P consumed and the conversions run beside other products.
 //
@@ -43,7 +46,7 @@ namespace ssd {
 namespace {
 
 constexpr int kBlk = kScanChunk;         // 128 tokens: the MMA's M
-constexpr int kThreads = 576;
+constexpr int kThreads = 608;
 constexpr uint32_t kPanel = kBlk * 128;  // 128 rows of 64 bf16
 constexpr uint32_t kPart = 32 * 128;     // 32 rows of 64 bf16
 
@@ -58,12 +61,12 @@ struct __align__(8) Bars {
     uint64_t full[kMaxBufs], empty[kMaxBufs];
     uint64_t s_full, p_full, o_full, o_free;
     uint64_t kt_full[2], kt_free[2];
-    uint64_t z_full, z_free, h_full, h_free;
+    uint64_t z_full, z_free, h_full, h_free, staged;
     uint64_t done;
 };
 
 struct TcParams {
-    CUtensorMap map[kScanRoles][3];  // q, k, v
+    CUtensorMap map[kScanRoles][4];  // q, k, v, out
     ScanLaunch s;
 };
 
@@ -80,8 +83,8 @@ struct Layout {
     static constexpr uint32_t kPartB = KP / 64 * kPart;  // one piece of 32 tokens
     static constexpr uint32_t OFF_H = OFF_PART + 2 * (kPieces - 1) * kPartB;
     static constexpr uint32_t OFF_TAB = OFF_H + (uint32_t)KP * VP * 2;
-    static constexpr uint32_t OFF_REV = OFF_TAB + 132 * 4;  // 16-byte aligned
-    static constexpr uint32_t OFF_BAR = OFF_REV + 32 * 4;
+    static constexpr uint32_t OFF_REV = OFF_TAB + 164 * 4;
+    static constexpr uint32_t OFF_BAR = OFF_REV + 160 * 4;
     static constexpr uint32_t OFF_MISC = OFF_BAR + (sizeof(Bars) + 15) / 16 * 16;
     static constexpr uint32_t OFF_ITEM = OFF_MISC + 16;
     static constexpr size_t kBytes = 1024 + OFF_ITEM + sizeof(ScanItem);
@@ -116,8 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sPart = sm + L::OFF_PART;  // [2][kPieces - 1] pieces of 32 tokens
     uint8_t* sH = sm + L::OFF_H;
-    float* sTab = reinterpret_cast<float*>(sm + L::OFF_TAB);  // l^0 .. l^128
-    float* sRev = reinterpret_cast<float*>(sm + L::OFF_REV);  // l^31 .. l^0
+    float* sTab = reinterpret_cast<float*>(sm + L::OFF_TAB) + 32;  // l^0 .. l^128; l^d = 0 for -32 <= d < 0
+    float* sRev = reinterpret_cast<float*>(sm + L::OFF_REV);       // l^127 .. l^0, then zeros for d = -1 .. -32
     Bars* bars = reinterpret_cast<Bars*>(sm + L::OFF_BAR);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::OFF_MISC);
     int* sAbort = reinterpret_cast<int*>(sm + L::OFF_MISC + 4);
@@ -162,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         tc::mbar_init(&bars->z_free, 8);
         tc::mbar_init(&bars->h_full, 8);
         tc::mbar_init(&bars->h_free, 1);
+        tc::mbar_init(&bars->staged, 8);
         tc::mbar_init(&bars->done, 1);
         *sAbort = 0;
         tc::fence_mbar_init();
@@ -170,11 +174,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         tc::tmem_alloc(sTmem, 512);
         tc::tmem_relinquish();
     }
-    if (threadIdx.x >= 64 && threadIdx.x - 64 <= kBlk) {
-        const int d = threadIdx.x - 64;
-        const float e = decay_power(la, d).x;
+    if (threadIdx.x >= 64 && threadIdx.x - 64 <= kBlk + 32) {
+        const int d = (int)threadIdx.x - 96;
+        const float e = d < 0 ? 0.f : decay_power(la, d).x;
         sTab[d] = e;
-        if (d < 32) sRev[31 - d] = e;
+        if (d < kBlk) sRev[kBlk - 1 - d] = e;
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -193,6 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     // first token (in the sequence) and tokens of the c-th chunk in scan order
     auto chunk_at = [&](int c) -> int { return it.t0 + (rev ? nch - 1 - c : c) * kBlk; };
     auto chunk_n = [&](int t) -> int { return min(kBlk, it.t1 - t); };
+    // a chunk of n tokens whose output leaves by plain stores: fp32, or a packed
+    // sequence's end, behind which the rows are another's
+    auto direct = [&](int n) -> bool { return R.out_f32 || (p.s.plan.packed && n < kBlk); };
 
     if (warp == 16) {
         if (lane == 0) {
@@ -224,134 +231,164 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             }
         }
     } else if (warp == 17) {
-        if (lane == 0) {
-            // ------------------------------------------------- MMA issue ----
-            constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);
-            constexpr uint32_t id_pv = tc::idesc_bf16_f32(128, VP, 0, 1);
-            constexpr uint32_t id_qh = tc::idesc_bf16_f32(128, VP, 0, kLaneV ? 0 : 1);
-            constexpr uint32_t id_z = tc::idesc_bf16_f32(128, kLaneV ? KP : VP, 1, 1);
-            const uint32_t base = tc::smem_u32(sm);
-            const uint64_t kmaj = tc::smem_desc_sw128(0, 16, 1024);         // rows contiguous along the contraction
-            const uint64_t mnmaj = tc::smem_desc_sw128(0, kPanel, 1024);    // contraction along the rows
-            const uint64_t partmn = tc::smem_desc_sw128(0, kPart, 1024);
-            auto at = [&](uint64_t d, uint32_t off) -> uint64_t { return tc::desc_adv(d, base + off); };
-            bool ok = true;
-            // Z (+)= (w o K)^T V over the 32 tokens of quarter u
-            auto quarter = [&](int c, int u, uint32_t k_off, uint32_t v_off) -> bool {
-                const uint32_t qn = 4u * c + u, s = qn & 1;
-                if (!wait(&bars->kt_full[s], (qn >> 1) & 1)) return false;
+        // ----------------------------------------------------- MMA issue ----
+        constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);
+        constexpr uint32_t id_pv = tc::idesc_bf16_f32(128, VP, 0, 1);
+        constexpr uint32_t id_qh = tc::idesc_bf16_f32(128, VP, 0, kLaneV ? 0 : 1);
+        constexpr uint32_t id_z = tc::idesc_bf16_f32(128, kLaneV ? KP : VP, 1, 1);
+        const uint32_t base = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const int chunks = __shfl_sync(0xffffffffu, nch, 0);
+        const uint64_t kmaj = tc::smem_desc_sw128(base, 16, 1024);       // rows contiguous along the contraction
+        const uint64_t mnmaj = tc::smem_desc_sw128(base, kPanel, 1024);  // contraction along the rows
+        const uint64_t partmn = tc::smem_desc_sw128(base + L::OFF_PART, kPart, 1024);
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t ph = c & 1, was = (c - 1) & 1;
+            const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
+            const uint64_t dkk = tc::desc_adv(kmaj, bk.off), dkm = tc::desc_adv(mnmaj, bk.off), dvm = tc::desc_adv(mnmaj, bv.off);
+            if (kOut) {
+                const auto bq = L::buf(c, 0, kOut);
+                const uint64_t dq = tc::desc_adv(kmaj, bq.off);
+                // the scores overwrite the P that the last P V read
+                ok = wait_warp(&bars->full[bq.i], bq.use & 1) && wait_warp(&bars->full[bk.i], bk.use & 1) &&
+                     (c == 0 || wait_warp(&bars->o_full, was));
+                if (!ok) break;
                 tc::tc_fence_after();
-#pragma unroll
-                for (int x = 0; x < kPieces; ++x) {
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        const uint64_t dk = x == 0 ? at(mnmaj, k_off + (2 * u + kk) * 2048)
-                                                   : at(partmn, L::OFF_PART + (s * (kPieces - 1) + x - 1) * L::kPartB +
-                                                                    kk * 2048);
-                        const uint64_t dv = at(mnmaj, v_off + (2 * u + kk) * 2048);
-                        tc::mma_ss(tmem + COL_Z, kLaneV ? dv : dk, kLaneV ? dk : dv, id_z,
-                                   (u > 0 || x > 0 || kk > 0) ? 1u : 0u);
-                    }
-                }
-                tc::mma_commit(&bars->kt_free[s]);
-                return true;
-            };
-            for (int c = 0; ok && c < nch; ++c) {
-                const uint32_t ph = c & 1, was = (c - 1) & 1;
-                const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
-                if (kOut) {
-                    const auto bq = L::buf(c, 0, kOut);
-                    // the scores overwrite the P that the last P V read
-                    ok = wait(&bars->full[bq.i], bq.use & 1) && wait(&bars->full[bk.i], bk.use & 1) &&
-                         (c == 0 || wait(&bars->o_full, was));
-                    if (!ok) break;
-                    tc::tc_fence_after();
+                if (tc::elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < KP / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                        tc::mma_ss(tmem + COL_S, at(kmaj, bq.off + off), at(kmaj, bk.off + off), id_s, kk > 0);
+                        tc::mma_ss(tm + COL_S, tc::desc_adv(dq, off), tc::desc_adv(dkk, off), id_s, kk > 0);
                     }
                     tc::mma_commit(&bars->s_full);
-                    ok = wait(&bars->h_full, ph) && (c == 0 || wait(&bars->o_free, was));
-                    if (!ok) break;
-                    tc::tc_fence_after();
+                }
+                __syncwarp();
+                ok = wait_warp(&bars->h_full, ph) && (c == 0 || wait_warp(&bars->o_free, was));
+                if (!ok) break;
+                tc::tc_fence_after();
+                if (tc::elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < KP / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                        const uint64_t dh = kLaneV ? at(kmaj, L::OFF_H + off) : at(mnmaj, L::OFF_H + kk * 2048);
-                        tc::mma_ss(tmem + COL_O2, at(kmaj, bq.off + off), dh, id_qh, kk > 0);
+                        const uint64_t dh = kLaneV ? tc::desc_adv(kmaj, L::OFF_H + off) : tc::desc_adv(mnmaj, L::OFF_H + kk * 2048);
+                        tc::mma_ss(tm + COL_O2, tc::desc_adv(dq, off), dh, id_qh, kk > 0);
                     }
                     tc::mma_commit(&bars->h_free);
                     tc::mma_commit(&bars->empty[bq.i]);
                 }
-                ok = wait(&bars->full[bv.i], bv.use & 1) && (c == 0 || wait(&bars->z_free, was)) &&
-                     quarter(c, 0, bk.off, bv.off) && quarter(c, 1, bk.off, bv.off);
+                __syncwarp();
+            }
+            ok = wait_warp(&bars->full[bv.i], bv.use & 1) && (c == 0 || wait_warp(&bars->z_free, was));
+            if (!ok) break;
+#pragma unroll 1
+            for (int u = 0; u < 4; ++u) {
+                // Z (+)= (w o K)^T V over the 32 tokens of quarter u
+                const uint32_t qn = 4u * c + u, s = qn & 1;
+                ok = wait_warp(&bars->kt_full[s], (qn >> 1) & 1);
                 if (!ok) break;
-                if (kOut) {
-                    ok = wait(&bars->p_full, ph);
+                tc::tc_fence_after();
+                if (tc::elect_one()) {
+                    const uint64_t dv = tc::desc_adv(dvm, u * 4096);
+                    const uint64_t dk = tc::desc_adv(dkm, u * 4096);
+                    const uint64_t dp = tc::desc_adv(partmn, s * (kPieces - 1) * L::kPartB);
+#pragma unroll
+                    for (int x = 0; x < kPieces; ++x) {
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const uint64_t a = x == 0 ? tc::desc_adv(dk, kk * 2048)
+                                                      : tc::desc_adv(dp, (x - 1) * L::kPartB + kk * 2048);
+                            const uint64_t b = tc::desc_adv(dv, kk * 2048);
+                            tc::mma_ss(tm + COL_Z, kLaneV ? b : a, kLaneV ? a : b, id_z, (u > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                        }
+                    }
+                    tc::mma_commit(&bars->kt_free[s]);
+                }
+                __syncwarp();
+                if (kOut && u == 1) {
+                    ok = wait_warp(&bars->p_full, ph);
                     if (!ok) break;
                     tc::tc_fence_after();
+                    if (tc::elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kBlk / 16; ++kk)
-                        tc::mma_ts(tmem + COL_O1, tmem + COL_S + kk * 8, at(mnmaj, bv.off + kk * 2048), id_pv, kk > 0);
-                    tc::mma_commit(&bars->o_full);
+                        for (int kk = 0; kk < kBlk / 16; ++kk)
+                            tc::mma_ts(tm + COL_O1, tm + COL_S + kk * 8, tc::desc_adv(dvm, kk * 2048), id_pv, kk > 0);
+                        tc::mma_commit(&bars->o_full);
+                    }
+                    __syncwarp();
                 }
-                ok = quarter(c, 2, bk.off, bv.off) && quarter(c, 3, bk.off, bv.off);
-                if (!ok) break;
+            }
+            if (!ok) break;
+            if (tc::elect_one()) {
                 tc::mma_commit(&bars->z_full);
-                tc::mma_commit(&bars->empty[bk.i]);
+                if (!kOut) tc::mma_commit(&bars->empty[bk.i]);  // else the output leaves through it first
                 tc::mma_commit(&bars->empty[bv.i]);
             }
+            __syncwarp();
+        }
+        if (!ok) fail();
+        // every product issued must be complete before TMEM is released
+        if (tc::elect_one()) tc::mma_commit(&bars->done);
+        __syncwarp();
+        tc::mbar_wait(&bars->done, 0, nullptr, 200000000ull);
+    } else if (warp == 18) {
+        if (kOut && lane == 0) {
+            // -------------------------------- the output tile, from K's place ----
+            bool ok = true;
+            for (int c = 0; c < nch; ++c) {
+                const int t = chunk_at(c), n = chunk_n(t);
+                const auto bk = L::buf(c, 1, kOut);
+                ok = wait(&bars->staged, c & 1);
+                if (!ok) break;
+                if (!direct(n)) {
+                    for (int x = 0; x < VP / 64; ++x)
+                        if (64 * x < V)
+                            tc::tma_store_4d(&p.map[it.role][3], sm + bk.off + x * kPanel, 64 * x, it.head,
+                                             (int)(it.row0 + t), it.batch);
+                    tc::bulk_commit();
+                    tc::bulk_wait_read<0>();
+                }
+                tc::mbar_arrive(&bars->empty[bk.i]);
+            }
             if (!ok) fail();
-            // every product issued must be complete before TMEM is released
-            tc::mma_commit(&bars->done);
-            tc::mbar_wait(&bars->done, 0, nullptr, 200000000ull);
         }
     } else if (warp < 4) {
         if (kOut) {
             // ------------------------------------- P = S o L, thread = row ----
             const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16) + COL_S;
-            const float4* tb = reinterpret_cast<const float4*>(rev ? sTab : sRev);
+            // l^|i-j| of row i against the columns of block jb: 32 consecutive
+            // entries of a table, neighbouring lanes one apart
+            const float* near = rev ? sTab - (32 * warp + lane) : sRev + kBlk - 1 - (32 * warp + lane);
+            const uint32_t diag = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
             bool ok = true;
+#pragma unroll 1
             for (int c = 0; c < nch; ++c) {
                 const int n = chunk_n(chunk_at(c));
                 ok = wait_warp(&bars->s_full, c & 1);
                 if (!ok) break;
                 tc::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int jb = 0; jb < 4; ++jb) {
+                    // the block's columns on the causal side and in the chunk
+                    uint32_t m = jb == warp ? diag : (rev ? jb > warp : jb < warp) ? 0xffffffffu : 0u;
+                    if (n < 32 * jb + 32) m &= n > 32 * jb ? 0xffffffffu >> (32 * jb + 32 - n) : 0u;
                     uint32_t r[16];
-                    if (rev ? jb >= warp : jb <= warp) {
+                    if (__any_sync(0xffffffffu, m != 0)) {
                         float s[32];
                         tc::tmem_ld32(ts + 32 * jb, s);
+                        const float* w = near + 32 * jb;
                         tc::tmem_ld_wait();
-                        if (jb == warp) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const int d = rev ? j - lane : lane - j;
-                                s[j] = d >= 0 ? s[j] * sTab[d & 31] : 0.f;
-                            }
-                        } else {
-                            // l^|i-j| = l^(to this block's near column) l^(from there)
-                            const float a = sTab[rev ? 32 * (jb - warp) - lane : 32 * (warp - jb) + lane - 31];
-                            const float2 a2 = make_float2(a, a);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float4 b = tb[j];
-                                const float2 lo = tc::mul2(make_float2(s[4 * j], s[4 * j + 1]), tc::mul2(a2, make_float2(b.x, b.y)));
-                                const float2 hi = tc::mul2(make_float2(s[4 * j + 2], s[4 * j + 3]), tc::mul2(a2, make_float2(b.z, b.w)));
-                                s[4 * j] = lo.x;
-                                s[4 * j + 1] = lo.y;
-                                s[4 * j + 2] = hi.x;
-                                s[4 * j + 3] = hi.y;
-                            }
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 v = tc::mul2(make_float2(s[2 * j], s[2 * j + 1]), make_float2(w[2 * j], w[2 * j + 1]));
+                            s[2 * j] = v.x;
+                            s[2 * j + 1] = v.y;
                         }
-                        // backwards, the columns behind a partial chunk are on the
-                        // causal side (whatever their rows of K hold)
-                        if (rev && n < 32 * jb + 32) {
+                        // a product with 0 would keep a NaN of a masked place
+                        if (!__all_sync(0xffffffffu, m == 0xffffffffu)) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (32 * jb + j >= n) s[j] = 0.f;
+                            for (int j = 0; j < 32; ++j) s[j] = (m >> j) & 1 ? s[j] : 0.f;
                         }
 #pragma unroll
                         for (int j = 0; j < 16; ++j) r[j] = tc::pack_bf16x2(s[2 * j], s[2 * j + 1]);
@@ -373,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         // ------------------------------------------------ w o K in pieces ----
         const int t = threadIdx.x - 128;
         bool ok = true;
+#pragma unroll 1
         for (int c = 0; ok && c < nch; ++c) {
             const int n = chunk_n(chunk_at(c));
             const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
@@ -400,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 const float2 w2 = make_float2(w, w), minus = make_float2(-1.f, -1.f);
                 uint8_t* krow = sm + bk.off + row * 128;
                 uint8_t* prow = sPart + s * (kPieces - 1) * L::kPartB + lane * 128;
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < KP / 64; ++x) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -449,10 +487,14 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             const float* src = from_init ? R.init + chain * K * V : p.s.states + it.slot_prev * K * V;
             const long long sk = from_init ? R.init_k : V, sv = from_init ? R.init_v : 1;
             const float mul = from_init ? R.init_scale : 1.f;
+            src += k_of(0) * sk + v_of(0) * sv;
+            const long long step = kLaneV ? sk : sv;
+            const int have = kLaneV ? (lr < V ? K - c0 : 0) : (lr < K ? V - c0 : 0);
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
-                if (k_of(c) < K && v_of(c) < V && SSD_INB(k_of(c) * sk + v_of(c) * sv, (long long)K * V))
-                    h[c] = src[k_of(c) * sk + v_of(c) * sv] * mul;
+            for (int c = 0; c < CH; ++c) {
+                if (c < have && SSD_INB(k_of(c) * sk + v_of(c) * sv, (long long)K * V)) h[c] = *src * mul;
+                src += step;
+            }
         }
         // H as an operand: [v][k] (lanes v) or [k][v]
         auto put_h = [&]() {
@@ -480,13 +522,19 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             if (!ok) break;
             tc::tc_fence_after();
             const float2 dec = n - 1 + off == kBlk ? whole : decay_power(la, n - 1 + off);
+            const float2 dx = make_float2(dec.x, dec.x), dy = make_float2(dec.y, dec.y);
 #pragma unroll
             for (int x = 0; x < CH / 32; ++x) {
                 float z[32];
                 tc::tmem_ld32(tl + COL_Z + c0 + 32 * x, z);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) h[32 * x + e] = fmaf(h[32 * x + e], dec.x, fmaf(h[32 * x + e], dec.y, z[e]));
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 o = make_float2(h[32 * x + e], h[32 * x + e + 1]);
+                    const float2 w = tc::fma2(o, dx, tc::fma2(o, dy, make_float2(z[e], z[e + 1])));
+                    h[32 * x + e] = w.x;
+                    h[32 * x + e + 1] = w.y;
+                }
             }
             tc::tc_fence_before();
             __syncwarp();
@@ -503,7 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 const float e = lr < n ? sTab[(rev ? n - 1 - lr : lr) + off] * R.out_scale : 0.f;
                 const long long row = (long long)it.batch * p.s.plan.T + it.row0 + t + lr;
                 const long long at0 = (row * H + it.head) * V;
-#pragma unroll
+                const bool plain = direct(n);
+                uint8_t* tile = sm + L::buf(c, 1, kOut).off + lr * 128;  // this chunk's K is consumed (z_full)
+#pragma unroll 1
                 for (int x = 0; x < VP / 32; ++x) {
                     const int col = half * (VP / 2) + 16 * x;
                     float a[16], b[16];
@@ -512,26 +562,39 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int q = 0; q < 16; ++q) a[q] = fmaf(e, b[q], R.out_scale * a[q]);
+                    uint32_t o[8];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int cy = col + 8 * y;
-                        if (lr < n && cy < V &&
-                            SSD_INB(at0 + cy + 7, (p.s.plan.packed ? 1LL : p.s.plan.B) * p.s.plan.T * H * V)) {
+                    for (int q = 0; q < 8; ++q) o[q] = tc::pack_bf16x2(a[2 * q], a[2 * q + 1]);
+                    if (!plain) {
+                        const int cc = (col & 63) >> 3;
+                        uint8_t* d = tile + (col >> 6) * kPanel;
+                        *reinterpret_cast<uint4*>(d + ((cc ^ (lr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(d + (((cc + 1) ^ (lr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int cy = col + 8 * y;
+                            if (lr >= n || cy >= V ||
+                                !SSD_INB(at0 + cy + 7, (p.s.plan.packed ? 1LL : p.s.plan.B) * p.s.plan.T * H * V))
+                                continue;
                             if (R.out_f32) {
-                                float4* o = reinterpret_cast<float4*>((float*)R.out + at0 + cy);
-                                o[0] = make_float4(a[8 * y], a[8 * y + 1], a[8 * y + 2], a[8 * y + 3]);
-                                o[1] = make_float4(a[8 * y + 4], a[8 * y + 5], a[8 * y + 6], a[8 * y + 7]);
+                                float4* f = reinterpret_cast<float4*>((float*)R.out + at0 + cy);
+                                f[0] = make_float4(a[8 * y], a[8 * y + 1], a[8 * y + 2], a[8 * y + 3]);
+                                f[1] = make_float4(a[8 * y + 4], a[8 * y + 5], a[8 * y + 6], a[8 * y + 7]);
                             } else {
                                 *reinterpret_cast<uint4*>((__nv_bfloat16*)R.out + at0 + cy) =
-                                    make_uint4(tc::pack_bf16x2(a[8 * y], a[8 * y + 1]), tc::pack_bf16x2(a[8 * y + 2], a[8 * y + 3]),
-                                               tc::pack_bf16x2(a[8 * y + 4], a[8 * y + 5]), tc::pack_bf16x2(a[8 * y + 6], a[8 * y + 7]));
+                                    make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                             }
                         }
                     }
                 }
                 tc::tc_fence_before();
+                tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->o_free);
+                if (lane == 0) {
+                    tc::mbar_arrive(&bars->o_free);
+                    tc::mbar_arrive(&bars->staged);
+                }
             }
             off = 1;
         }
@@ -546,9 +609,14 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             mul = R.fin_scale * (rev && it.len > 0 ? decay_power(la, 1).x : 1.f);
         }
         if (ok && dst && holds && SSD_INB(kOut ? chain : it.slot, kOut ? chains : p.s.plan.slots())) {
+            dst += (long long)k_of(0) * V + v_of(0);
+            const int step = kLaneV ? V : 1;
+            const int have = kLaneV ? (lr < V ? K - c0 : 0) : (lr < K ? V - c0 : 0);
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
-                if (k_of(c) < K && v_of(c) < V) dst[(long long)k_of(c) * V + v_of(c)] = h[c] * mul;
+            for (int c = 0; c < CH; ++c) {
+                if (c < have) *dst = h[c] * mul;
+                dst += step;
+            }
         }
     }
     tc::tc_fence_before();
@@ -568,6 +636,9 @@ cudaError_t role_maps(const ScanRole& r, const ScanPlan& p, CUtensorMap* m) {
     for (int i = 0; i < 3 && e == cudaSuccess; ++i)
         e = make_tmap_bf16_rows(&m[i], t[i]->p, i == 2 ? r.V : r.K, p.H / t[i]->share, p.T, p.packed ? 1 : p.B,
                                 t[i]->head, t[i]->token, t[i]->batch, kBlk);
+    if (e == cudaSuccess && !r.out_f32)
+        e = make_tmap_bf16_rows(&m[3], r.out, r.V, p.H, p.T, p.packed ? 1 : p.B, r.V, (long long)p.H * r.V,
+                                (long long)p.T * p.H * r.V, kBlk);
     return e;
 }
 
@@ -593,7 +664,7 @@ cudaError_t launch_dims(const TcParams& p, bool state_only, cudaStream_t st) {
 
 bool scan_tc_supported(const ScanRole& r, const ScanPlan& p, bool bf16) {
     if (!bf16 || r.K > 128 || r.V > 128 || r.K % 8 != 0 || r.V % 8 != 0) return false;
-    CUtensorMap m[3];
+    CUtensorMap m[4];
     return role_maps(r, p, m) == cudaSuccess;
 }
 

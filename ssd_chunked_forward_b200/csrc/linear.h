@@ -180,7 +180,9 @@ __device__ inline void scan_item_tokens(ScanItem& r, int seg_tokens, int reverse
 // exp(decay * n) as an unevaluated sum of two fp32 numbers: a long chain
 // multiplies its state by the same factor at every chunk, and the error of one
 // rounded factor would grow with the number of chunks the state remembers.
-__device__ inline float2 decay_power(float decay, int n) {
+// Not inlined: a 64-bit exponential is long, and the scan's loops have to stay
+// in the instruction cache.
+static __device__ __noinline__ float2 decay_power(float decay, int n) {
     const double e = n == 0 ? 1.0 : exp((double)decay * n);
     const float hi = (float)e;
     return make_float2(hi, (float)(e - (double)hi));

@@ -239,6 +239,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// true in one lane of a converged warp.  Code that the whole warp reaches and one
+// elected lane executes keeps descriptors in uniform registers, where the MMA
+// instructions take them.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
 // arrive on an mbarrier once every MMA issued so far by this thread completes
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     asm volatile(
