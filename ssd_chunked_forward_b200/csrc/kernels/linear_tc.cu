@@ -5,34 +5,39 @@
 // order.  With positions i, j in a chunk of n tokens, l = exp(decay) and H the
 // fp32 state entering it:
 //     S   = Q K^T                                   scores
-//     P   = S o L,  L_ij = l^|i-j| on the causal side, else 0    (bf16, in TMEM)
-//     out = out_scale (P V + diag(l^(i+1)) Q H)     two accumulators, joined in fp32
+//     P   = S o L,  L_ij = out_scale l^|i-j| on the causal side, else 0   (bf16, in TMEM)
+//     out = P V + out_scale diag(l^(i+1)) Q H       two accumulators, joined in fp32
 //     Z   = (w o K)^T V,  w_j = l^(n-1-j)           the chunk's own state
 //     H  <- l^n H + Z                               in registers, fp32
-// and the mirror image for a scan backwards.  No factor exceeds 1: L is built
-// from two factors <= 1 per 32 x 32 block, one table of powers made in 64 bits.
+// and the mirror image for a scan backwards.  No power of l has a negative
+// exponent; a table of them is made in 64 bits.
 //
 // Precision.  P, and H as an operand, are rounded to bf16 (their errors are
 // those of the result's own rounding).  The state itself is fp32 and outlives
-// the call, so w o K must not lose bits: it enters the product as kPieces bf16
-// numbers whose sum is the fp32 product: 3 leave an error below 2^-24 and are
-// used where the state is a result, 2 (below 2^-17) where it only enters
-// outputs.  l^n multiplies H at every chunk and is kept as a sum of two fp32
-// numbers, or its rounding would grow with the number of chunks.
+// the call, so w o K must not lose bits: it (or w o V, whichever is 64 wide)
+// enters the product as kPieces bf16 numbers, the first ones its leading bits,
+// the last one rounded: 3 hold the fp32 product whole and are used where the
+// state is a result, 2 (error below 2^-17) where it only enters outputs.
+// l^n multiplies H at every chunk and is kept as a sum of two fp32 numbers, or
+// its rounding would grow with the number of chunks.
 //
-// Warp roles (608 threads):
+// Warp roles (640 threads):
 //   0-3    scores -> P (thread = row i)
-//   4-7    w o K: the first piece in K's own place in shared memory once the
-//          scores are done, the others in two buffers of 32 tokens in turn;
-//          rows behind a partial chunk's end become zeros there, in V too (with
-//          packed sequences they hold the next sequence's tokens)
+//   4-7    w o K or w o V in pieces: parts of 16 tokens, each a warp's own (one part
+//          shared by four warps took as long, most of it latency), two parts to a
+//          buffer and a hand-over (one each: the MMA warp spent its time waiting); rows
+//          behind a partial chunk's end become zeros in K and V (with packed
+//          sequences they hold the next sequence's tokens)
 //   8-15   state and output (two warps per TMEM lane quadrant)
-//   16     TMA loads; 17  TMEM, MMA issue
-//   18     TMA stores: the output tile takes the place of the chunk's K in shared
-//          memory (plain stores of rows by their threads touch 32 lines each: they
-//          kept the load/store unit busy for 2000 of a chunk's cycles)
-// MMA order per chunk: S, Q H, half of Z, P V, the other half of Z, so that the
-// next chunk's S finds P consumed and the conversions run beside other products.
+//   16     TMA loads
+//   17     TMEM; issues S, Q H and P V.  V = 64 leaves TMEM for a second score
+//          buffer: the next chunk's S goes first, so that P is made a chunk ahead
+//   18     TMA stores of output tiles (plain stores of rows by their threads touch
+//          32 lines each: they kept the load/store unit busy for 2000 cycles a chunk)
+//   19     issues Z.  An MMA of 128 rows and 16 tokens takes 43 + N / 2 cycles with
+//          both operands in shared memory, 10 + N / 2 with P in TMEM (measured): a
+//          chunk's products are 3600 cycles at K = 128, V = 64, 4900 at 128, 128, with
+//          the loads' share of HBM at 4100 and 5500.
 //
 // With V = 128 the lanes of Z are the state's columns (v), else its rows (k): an
 // MMA takes 128 rows, and the other order would waste half of them.
@@ -46,23 +51,21 @@ namespace ssd {
 namespace {
 
 constexpr int kBlk = kScanChunk;         // 128 tokens: the MMA's M
-constexpr int kThreads = 608;
+constexpr int kThreads = 640;
 constexpr uint32_t kPanel = kBlk * 128;  // 128 rows of 64 bf16
-constexpr uint32_t kPart = 32 * 128;     // 32 rows of 64 bf16
+constexpr int kPartT = 16;               // tokens of a part: the MMA's K
+constexpr uint32_t kPartPanel = kPartT * 128;
+constexpr int kGroups = kBlk / (2 * kPartT);  // a chunk's groups of two parts
 
-// TMEM columns
-constexpr uint32_t COL_S = 0;    // scores, then P in the first 64
-constexpr uint32_t COL_O1 = 128;
-constexpr uint32_t COL_O2 = 256;
-constexpr uint32_t COL_Z = 384;
-
-constexpr int kMaxBufs = 12;
+constexpr int kMaxBufs = 9, kMaxGroupBufs = 4;
 struct __align__(8) Bars {
     uint64_t full[kMaxBufs], empty[kMaxBufs];
-    uint64_t s_full, p_full, o_full, o_free;
-    uint64_t kt_full[2], kt_free[2];
-    uint64_t z_full, z_free, h_full, h_free, staged;
-    uint64_t done;
+    // s_full alternates even with one score buffer: the next chunk's S may be done
+    // before the warps that make the pieces have seen this one's
+    uint64_t s_full[2], p_full[2], o_full, o_free;
+    uint64_t x_full[kMaxGroupBufs], x_free[kMaxGroupBufs], clean;
+    uint64_t z_full[2], z_free[2], h_full, h_free, staged, stored;
+    uint64_t done, z_done;
 };
 
 struct TcParams {
@@ -70,25 +73,41 @@ struct TcParams {
     ScanLaunch s;
 };
 
-// Shared memory of a variant.  K = V = 128: a ring of five tiles in the order
-// q, k, v, q, ... (a whole second chunk does not fit); else whole chunks.
+// Shared and tensor memory of a variant.  K = V = 128: a ring of five tiles in
+// the order q, k, v, q, ... (a whole second chunk does not fit); the first piece
+// of w o K goes into K's own place once the scores are done, and the output
+// tile into V's.  The others hold whole chunks, all pieces and an output tile.
 template <int KP, int VP, int kPieces>
 struct Layout {
     static constexpr bool kRing = KP == 128 && VP == 128;
     static constexpr uint32_t kKB = KP / 64 * kPanel, kVB = VP / 64 * kPanel;
     static constexpr uint32_t kChunk = 2 * kKB + kVB;
-    static constexpr int kStages = kRing ? 0 : KP == 128 ? 2 : VP == 128 ? 3 : 4;
+    static constexpr int kStages = kRing ? 0 : KP == 64 && VP == 64 ? 3 : 2;
     static constexpr int kBufs = kRing ? 5 : 3 * kStages;
+    // the scaled operand and its parts: pieces first .. kPieces - 1 in buffers
+    static constexpr bool kScaleV = VP == 64;
+    static constexpr int kXW = kRing ? 128 : 64;
+    static constexpr int kFirst = kRing ? 1 : 0;
+    static constexpr uint32_t kPieceB = kXW / 64 * kPartPanel;
+    static constexpr uint32_t kPartB = (kPieces - kFirst) * kPieceB;
+    static constexpr int kGroupBufs = kRing || KP == 128 ? 2 : 4;
     static constexpr uint32_t OFF_PART = kRing ? 5 * 2 * kPanel : kStages * kChunk;
-    static constexpr uint32_t kPartB = KP / 64 * kPart;  // one piece of 32 tokens
-    static constexpr uint32_t OFF_H = OFF_PART + 2 * (kPieces - 1) * kPartB;
-    static constexpr uint32_t OFF_TAB = OFF_H + (uint32_t)KP * VP * 2;
-    static constexpr uint32_t OFF_REV = OFF_TAB + 164 * 4;
-    static constexpr uint32_t OFF_BAR = OFF_REV + 160 * 4;
+    static constexpr uint32_t OFF_H = OFF_PART + 2 * kGroupBufs * kPartB;
+    static constexpr uint32_t OFF_OUT = OFF_H + (uint32_t)KP * VP * 2;
+    static constexpr uint32_t OFF_TAB = OFF_OUT + (kRing ? 0 : kVB);
+    static constexpr uint32_t OFF_NEAR = OFF_TAB + 132 * 4;
+    static constexpr uint32_t OFF_DEC = OFF_NEAR + 160 * 4;
+    static constexpr uint32_t OFF_BAR = OFF_DEC + 4 * 8;
     static constexpr uint32_t OFF_MISC = OFF_BAR + (sizeof(Bars) + 15) / 16 * 16;
     static constexpr uint32_t OFF_ITEM = OFF_MISC + 16;
     static constexpr size_t kBytes = 1024 + OFF_ITEM + sizeof(ScanItem);
     static_assert(kBytes <= 232448, "shared memory above the 227 KB per-block limit");
+    static_assert(OFF_PART % 1024 == 0 && OFF_H % 1024 == 0 && OFF_OUT % 1024 == 0, "swizzled tiles start on 1024 bytes");
+
+    // TMEM columns: scores (P in their first 64), P V, Q H, Z
+    static constexpr int kS = VP == 64 ? 2 : 1;
+    static constexpr int kZ = VP == 64 ? 2 : 1;
+    static constexpr uint32_t COL_S = 0, COL_O1 = 128 * kS, COL_O2 = COL_O1 + VP, COL_Z = 384;
 
     // buffer, its use count and its place, of tile `which` (0 q, 1 k, 2 v) of chunk c;
     // a state-only scan loads no q
@@ -110,6 +129,17 @@ struct Layout {
     }
 };
 
+// The bounded wait of tc_common.cuh without its out-of-line part: a call would
+// spill the state that the warps hold in registers.
+__device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+    for (;;) {
+        if (tc::mbar_try_wait_sleep(bar, parity, 500000u)) return true;
+        if (*abort || tc::globaltimer_ns() - t0 > 2000000000ull) return false;
+    }
+}
+
 template <int KP, int VP, bool kOut, int kPieces>
 __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ TcParams p) {
     using L = Layout<KP, VP, kPieces>;
@@ -117,10 +147,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     constexpr int CH = kLaneV ? KP / 2 : 32;   // state columns of a thread
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sPart = sm + L::OFF_PART;  // [2][kPieces - 1] pieces of 32 tokens
     uint8_t* sH = sm + L::OFF_H;
-    float* sTab = reinterpret_cast<float*>(sm + L::OFF_TAB) + 32;  // l^0 .. l^128; l^d = 0 for -32 <= d < 0
-    float* sRev = reinterpret_cast<float*>(sm + L::OFF_REV);       // l^127 .. l^0, then zeros for d = -1 .. -32
+    float* sTab = reinterpret_cast<float*>(sm + L::OFF_TAB);  // l^0 .. l^128
+    // out_scale l^d for the scores (0 for d < 0): d = 127 .. -32, or -32 .. 127 backwards
+    float* sNear = reinterpret_cast<float*>(sm + L::OFF_NEAR);
+    // what H is multiplied by in a whole chunk, in the first and in the last one
+    float2* sDec = reinterpret_cast<float2*>(sm + L::OFF_DEC);
     Bars* bars = reinterpret_cast<Bars*>(sm + L::OFF_BAR);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::OFF_MISC);
     int* sAbort = reinterpret_cast<int*>(sm + L::OFF_MISC + 4);
@@ -140,6 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     const ScanRole& R = p.s.role[it.role];
     const int K = R.K, V = R.V;
     const bool rev = R.reverse != 0;
+    const float out_scale = R.out_scale;
+    const bool out_f32 = R.out_f32 != 0, packed = p.s.plan.packed != 0;
     const float la = p.s.decay[it.head];
     const int H = p.s.plan.H;
     const long long chain = (long long)it.seq * H + it.head;
@@ -150,22 +184,33 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
 
     if (threadIdx.x == 32) {
         for (int i = 0; i < L::kBufs; ++i) {
+            // a tile's place is free again when each of its products is done (q: Q H
+            // after S; k: S, Z; v: P V, Z) and, in the ring, v's output has left
+            int users = 1;
+            if (kOut && !L::kRing) users = i % 3 == 0 ? 1 : 2;
             tc::mbar_init(&bars->full[i], 1);
-            tc::mbar_init(&bars->empty[i], 1);
+            tc::mbar_init(&bars->empty[i], kOut && L::kRing ? 3 : users);
         }
-        tc::mbar_init(&bars->s_full, 1);
-        tc::mbar_init(&bars->p_full, 4);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bars->s_full[i], 1);
+            tc::mbar_init(&bars->p_full[i], 4);
+        }
         tc::mbar_init(&bars->o_full, 1);
         tc::mbar_init(&bars->o_free, 8);
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bars->kt_full[i], 4);
-            tc::mbar_init(&bars->kt_free[i], 1);
+        for (int i = 0; i < kMaxGroupBufs; ++i) {
+            tc::mbar_init(&bars->x_full[i], 2);
+            tc::mbar_init(&bars->x_free[i], 1);
         }
-        tc::mbar_init(&bars->z_full, 1);
-        tc::mbar_init(&bars->z_free, 8);
+        tc::mbar_init(&bars->clean, 4);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bars->z_full[i], 1);
+            tc::mbar_init(&bars->z_free[i], 8);
+        }
         tc::mbar_init(&bars->h_full, 8);
         tc::mbar_init(&bars->h_free, 1);
         tc::mbar_init(&bars->staged, 8);
+        tc::mbar_init(&bars->stored, 1);
+        tc::mbar_init(&bars->z_done, 1);
         tc::mbar_init(&bars->done, 1);
         *sAbort = 0;
         tc::fence_mbar_init();
@@ -177,29 +222,50 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     if (threadIdx.x >= 64 && threadIdx.x - 64 <= kBlk + 32) {
         const int d = (int)threadIdx.x - 96;
         const float e = d < 0 ? 0.f : decay_power(la, d).x;
-        sTab[d] = e;
-        if (d < kBlk) sRev[kBlk - 1 - d] = e;
+        if (d >= 0) sTab[d] = e;
+        if (d < kBlk) sNear[rev ? d + 32 : kBlk - 1 - d] = e * out_scale;
+    }
+    // a backward scan's initial state meets its first token undecayed
+    const int off0 = it.seg == 0 && rev ? 0 : 1;
+    if (threadIdx.x >= 256 && threadIdx.x < 259) {
+        const int i = threadIdx.x - 256;
+        const int at_end = (span - 1) % kBlk + 1;  // tokens of the sequence's partial chunk, or 128
+        const int n = nch == 0 || i == 0 ? kBlk : i == 1 ? (rev || nch == 1 ? at_end : kBlk) : (rev && nch > 1 ? kBlk : at_end);
+        sDec[i] = decay_power(la, i == 1 || (i == 2 && nch == 1) ? n - 1 + off0 : n);
     }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *sTmem;
+    // 64 state columns in a thread do not fit beside the rest in the 96 registers
+    // that 19 warps leave each: those warps take 24 from the scores' and pieces'
+    auto give = [] { if constexpr (CH == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); };
+    auto take = [] { if constexpr (CH == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;"); };
 
     auto fail = [&]() {
         *reinterpret_cast<volatile int*>(sAbort) = 1;
         atomicExch(p.s.status, kDevTimeout);
     };
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return tc::mbar_wait(bar, parity, abort_v); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_here(bar, parity, abort_v); };
     // the same decision in every lane: what follows is executed by whole warps
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_v));
+        return __all_sync(0xffffffffu, wait_here(bar, parity, abort_v));
     };
     // first token (in the sequence) and tokens of the c-th chunk in scan order
+    // Arrivals on a tile's empty barrier once the products issued so far are done.
+    // Buffers of the ring hold q, k and v in turn and expect three arrivals each
+    // time: Q H makes q's three, S one and Z two of k's, P V, Z and the output's
+    // store one each of v's.
+    auto release = [&](uint32_t e, uint32_t buf, int in_ring) {
+        tc::mma_commit_if(e, &bars->empty[buf]);
+        if (kOut && L::kRing)
+            for (int i = 1; i < in_ring; ++i) tc::mma_commit_if(e, &bars->empty[buf]);
+    };
     auto chunk_at = [&](int c) -> int { return it.t0 + (rev ? nch - 1 - c : c) * kBlk; };
     auto chunk_n = [&](int t) -> int { return min(kBlk, it.t1 - t); };
     // a chunk of n tokens whose output leaves by plain stores: fp32, or a packed
     // sequence's end, behind which the rows are another's
-    auto direct = [&](int n) -> bool { return R.out_f32 || (p.s.plan.packed && n < kBlk); };
+    auto direct = [&](int n) -> bool { return out_f32 || (packed && n < kBlk); };
 
     if (warp == 16) {
         if (lane == 0) {
@@ -235,137 +301,160 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);
         constexpr uint32_t id_pv = tc::idesc_bf16_f32(128, VP, 0, 1);
         constexpr uint32_t id_qh = tc::idesc_bf16_f32(128, VP, 0, kLaneV ? 0 : 1);
-        constexpr uint32_t id_z = tc::idesc_bf16_f32(128, kLaneV ? KP : VP, 1, 1);
         const uint32_t base = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const int chunks = __shfl_sync(0xffffffffu, nch, 0);
         const uint64_t kmaj = tc::smem_desc_sw128(base, 16, 1024);       // rows contiguous along the contraction
         const uint64_t mnmaj = tc::smem_desc_sw128(base, kPanel, 1024);  // contraction along the rows
-        const uint64_t partmn = tc::smem_desc_sw128(base + L::OFF_PART, kPart, 1024);
+        const uint32_t lead = tc::elect_one();
         bool ok = true;
+        // S of chunk c
+        auto scores = [&](int c) -> bool {
+            const auto bq = L::buf(c, 0, kOut), bk = L::buf(c, 1, kOut);
+            if (!(wait_warp(&bars->full[bq.i], bq.use & 1) && wait_warp(&bars->full[bk.i], bk.use & 1))) return false;
+            // they overwrite the P that P V of the chunk kS before read
+            if (c >= L::kS && !wait_warp(&bars->o_full, (c - L::kS) & 1)) return false;
+            tc::tc_fence_after();
+            {
+                const uint64_t dq = tc::desc_adv(kmaj, bq.off), dk = tc::desc_adv(kmaj, bk.off);
+                const uint32_t d = tm + L::COL_S + (c % L::kS) * 128;
+#pragma unroll
+                for (int kk = 0; kk < KP / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
+                    tc::mma_ss_if(lead, d, tc::desc_adv(dq, off), tc::desc_adv(dk, off), id_s, kk > 0);
+                }
+                tc::mma_commit_if(lead, &bars->s_full[c & 1]);
+                release(lead, bk.i, 1);
+            }
+            return true;
+        };
+        if (kOut && L::kS == 2 && chunks > 0) ok = scores(0);
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            const uint32_t ph = c & 1, was = (c - 1) & 1;
-            const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
-            const uint64_t dkk = tc::desc_adv(kmaj, bk.off), dkm = tc::desc_adv(mnmaj, bk.off), dvm = tc::desc_adv(mnmaj, bv.off);
-            if (kOut) {
+        for (int c = 0; kOut && ok && c < chunks; ++c) {
+            if (L::kS == 1) ok = scores(c);
+            else if (c + 1 < chunks) ok = scores(c + 1);
+            // Q H
+            ok = ok && wait_warp(&bars->h_full, c & 1) && (c == 0 || wait_warp(&bars->o_free, (c - 1) & 1));
+            if (!ok) break;
+            tc::tc_fence_after();
+            const auto bv = L::buf(c, 2, kOut);
+            {
                 const auto bq = L::buf(c, 0, kOut);
                 const uint64_t dq = tc::desc_adv(kmaj, bq.off);
-                // the scores overwrite the P that the last P V read
-                ok = wait_warp(&bars->full[bq.i], bq.use & 1) && wait_warp(&bars->full[bk.i], bk.use & 1) &&
-                     (c == 0 || wait_warp(&bars->o_full, was));
-                if (!ok) break;
-                tc::tc_fence_after();
-                if (tc::elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < KP / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                        tc::mma_ss(tm + COL_S, tc::desc_adv(dq, off), tc::desc_adv(dkk, off), id_s, kk > 0);
-                    }
-                    tc::mma_commit(&bars->s_full);
+                for (int kk = 0; kk < KP / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
+                    const uint64_t dh = kLaneV ? tc::desc_adv(kmaj, L::OFF_H + off) : tc::desc_adv(mnmaj, L::OFF_H + kk * 2048);
+                    tc::mma_ss_if(lead, tm + L::COL_O2, tc::desc_adv(dq, off), dh, id_qh, kk > 0);
                 }
-                __syncwarp();
-                ok = wait_warp(&bars->h_full, ph) && (c == 0 || wait_warp(&bars->o_free, was));
-                if (!ok) break;
-                tc::tc_fence_after();
-                if (tc::elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < KP / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                        const uint64_t dh = kLaneV ? tc::desc_adv(kmaj, L::OFF_H + off) : tc::desc_adv(mnmaj, L::OFF_H + kk * 2048);
-                        tc::mma_ss(tm + COL_O2, tc::desc_adv(dq, off), dh, id_qh, kk > 0);
-                    }
-                    tc::mma_commit(&bars->h_free);
-                    tc::mma_commit(&bars->empty[bq.i]);
-                }
-                __syncwarp();
+                tc::mma_commit_if(lead, &bars->h_free);
+                release(lead, bq.i, 3);
             }
-            ok = wait_warp(&bars->full[bv.i], bv.use & 1) && (c == 0 || wait_warp(&bars->z_free, was));
+            // P V
+            ok = wait_warp(&bars->full[bv.i], bv.use & 1) && wait_warp(&bars->p_full[c % L::kS], (c / L::kS) & 1) &&
+                 (chunk_n(chunk_at(c)) == kBlk || wait_warp(&bars->clean, 0));
             if (!ok) break;
-#pragma unroll 1
-            for (int u = 0; u < 4; ++u) {
-                // Z (+)= (w o K)^T V over the 32 tokens of quarter u
-                const uint32_t qn = 4u * c + u, s = qn & 1;
-                ok = wait_warp(&bars->kt_full[s], (qn >> 1) & 1);
-                if (!ok) break;
-                tc::tc_fence_after();
-                if (tc::elect_one()) {
-                    const uint64_t dv = tc::desc_adv(dvm, u * 4096);
-                    const uint64_t dk = tc::desc_adv(dkm, u * 4096);
-                    const uint64_t dp = tc::desc_adv(partmn, s * (kPieces - 1) * L::kPartB);
+            tc::tc_fence_after();
+            {
+                const uint64_t dv = tc::desc_adv(mnmaj, bv.off);
+                const uint32_t a = tm + L::COL_S + (c % L::kS) * 128;
 #pragma unroll
-                    for (int x = 0; x < kPieces; ++x) {
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk) {
-                            const uint64_t a = x == 0 ? tc::desc_adv(dk, kk * 2048)
-                                                      : tc::desc_adv(dp, (x - 1) * L::kPartB + kk * 2048);
-                            const uint64_t b = tc::desc_adv(dv, kk * 2048);
-                            tc::mma_ss(tm + COL_Z, kLaneV ? b : a, kLaneV ? a : b, id_z, (u > 0 || x > 0 || kk > 0) ? 1u : 0u);
-                        }
-                    }
-                    tc::mma_commit(&bars->kt_free[s]);
-                }
-                __syncwarp();
-                if (kOut && u == 1) {
-                    ok = wait_warp(&bars->p_full, ph);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    if (tc::elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < kBlk / 16; ++kk)
-                            tc::mma_ts(tm + COL_O1, tm + COL_S + kk * 8, tc::desc_adv(dvm, kk * 2048), id_pv, kk > 0);
-                        tc::mma_commit(&bars->o_full);
-                    }
-                    __syncwarp();
-                }
+                for (int kk = 0; kk < kBlk / 16; ++kk)
+                    tc::mma_ts_if(lead, tm + L::COL_O1, a + kk * 8, tc::desc_adv(dv, kk * 2048), id_pv, kk > 0);
+                tc::mma_commit_if(lead, &bars->o_full);
+                release(lead, bv.i, 1);
             }
-            if (!ok) break;
-            if (tc::elect_one()) {
-                tc::mma_commit(&bars->z_full);
-                if (!kOut) tc::mma_commit(&bars->empty[bk.i]);  // else the output leaves through it first
-                tc::mma_commit(&bars->empty[bv.i]);
-            }
-            __syncwarp();
         }
         if (!ok) fail();
         // every product issued must be complete before TMEM is released
-        if (tc::elect_one()) tc::mma_commit(&bars->done);
-        __syncwarp();
+        tc::mma_commit_if(lead, &bars->done);
         tc::mbar_wait(&bars->done, 0, nullptr, 200000000ull);
+    } else if (warp == 19) {
+        // ------------------------------------------------- Z = (w o K)^T V ----
+        constexpr uint32_t id_z = tc::idesc_bf16_f32(128, L::kXW, 1, 1);
+        const uint32_t base = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const int chunks = __shfl_sync(0xffffffffu, nch, 0);
+        const uint64_t mnmaj = tc::smem_desc_sw128(base, kPanel, 1024);
+        const uint64_t partmn = tc::smem_desc_sw128(base + L::OFF_PART, kPartPanel, 1024);
+        const uint32_t lead = tc::elect_one();
+        bool ok = true;
+#pragma unroll 1
+        for (int c = 0; ok && c < chunks; ++c) {
+            const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
+            ok = wait_warp(&bars->full[bk.i], bk.use & 1) && wait_warp(&bars->full[bv.i], bv.use & 1) &&
+                 (c < L::kZ || wait_warp(&bars->z_free[c % L::kZ], (c / L::kZ - 1) & 1)) &&
+                 (chunk_n(chunk_at(c)) == kBlk || wait_warp(&bars->clean, 0));
+            if (!ok) break;
+            tc::tc_fence_after();
+            // the operand that stays whole fills the MMA's rows
+            const uint64_t whole = tc::desc_adv(mnmaj, L::kScaleV ? bk.off : bv.off);
+            const uint64_t inplace = tc::desc_adv(mnmaj, bk.off);
+            const uint32_t z = tm + L::COL_Z + (c % L::kZ) * 64;
+#pragma unroll 1
+            for (int u = 0; u < kGroups; ++u) {
+                const uint32_t g = (uint32_t)kGroups * c + u, s = g % L::kGroupBufs;
+                ok = wait_warp(&bars->x_full[s], (g / L::kGroupBufs) & 1);
+                if (!ok) break;
+                const uint64_t da = tc::desc_adv(whole, u * 2 * kPartPanel);
+                const uint64_t di = tc::desc_adv(inplace, u * 2 * kPartPanel);
+                const uint64_t dx = tc::desc_adv(partmn, s * 2 * L::kPartB);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int x = 0; x < kPieces; ++x)
+                        tc::mma_ss_if(lead, z, tc::desc_adv(da, i * kPartPanel),
+                                      x < L::kFirst ? tc::desc_adv(di, i * kPartPanel)
+                                                    : tc::desc_adv(dx, i * L::kPartB + (x - L::kFirst) * L::kPieceB),
+                                      id_z, (u > 0 || i > 0 || x > 0) ? 1u : 0u);
+                tc::mma_commit_if(lead, &bars->x_free[s]);
+            }
+            if (!ok) break;
+            tc::mma_commit_if(lead, &bars->z_full[c % L::kZ]);
+            release(lead, bk.i, 2);
+            release(lead, bv.i, 1);
+        }
+        if (!ok) fail();
+        tc::mma_commit_if(lead, &bars->z_done);
+        tc::mbar_wait(&bars->z_done, 0, nullptr, 200000000ull);
     } else if (warp == 18) {
         if (kOut && lane == 0) {
-            // -------------------------------- the output tile, from K's place ----
+            // ---------------------------------------------------- TMA stores ----
             bool ok = true;
             for (int c = 0; c < nch; ++c) {
-                const int t = chunk_at(c), n = chunk_n(t);
-                const auto bk = L::buf(c, 1, kOut);
+                const int t = chunk_at(c);
+                const auto bv = L::buf(c, 2, kOut);
                 ok = wait(&bars->staged, c & 1);
                 if (!ok) break;
-                if (!direct(n)) {
+                if (!direct(chunk_n(t))) {
+                    const uint8_t* tile = sm + (L::kRing ? bv.off : L::OFF_OUT);
                     for (int x = 0; x < VP / 64; ++x)
                         if (64 * x < V)
-                            tc::tma_store_4d(&p.map[it.role][3], sm + bk.off + x * kPanel, 64 * x, it.head,
-                                             (int)(it.row0 + t), it.batch);
+                            tc::tma_store_4d(&p.map[it.role][3], tile + x * kPanel, 64 * x, it.head, (int)(it.row0 + t),
+                                             it.batch);
                     tc::bulk_commit();
                     tc::bulk_wait_read<0>();
                 }
-                tc::mbar_arrive(&bars->empty[bk.i]);
+                if (L::kRing) tc::mbar_arrive(&bars->empty[bv.i]);
+                tc::mbar_arrive(&bars->stored);
             }
             if (!ok) fail();
         }
     } else if (warp < 4) {
+        give();
         if (kOut) {
             // ------------------------------------- P = S o L, thread = row ----
-            const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16) + COL_S;
-            // l^|i-j| of row i against the columns of block jb: 32 consecutive
+            const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16) + L::COL_S;
+            // out_scale l^|i-j| of row i against the columns of block jb: 32 consecutive
             // entries of a table, neighbouring lanes one apart
-            const float* near = rev ? sTab - (32 * warp + lane) : sRev + kBlk - 1 - (32 * warp + lane);
+            const float* near = sNear + (rev ? 32 : kBlk - 1) - (32 * warp + lane);
             const uint32_t diag = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
             bool ok = true;
 #pragma unroll 1
             for (int c = 0; c < nch; ++c) {
                 const int n = chunk_n(chunk_at(c));
-                ok = wait_warp(&bars->s_full, c & 1);
+                const uint32_t tc0 = ts + (c % L::kS) * 128;
+                ok = wait_warp(&bars->s_full[c & 1], (c >> 1) & 1);
                 if (!ok) break;
                 tc::tc_fence_after();
 #pragma unroll 1
@@ -376,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     uint32_t r[16];
                     if (__any_sync(0xffffffffu, m != 0)) {
                         float s[32];
-                        tc::tmem_ld32(ts + 32 * jb, s);
+                        tc::tmem_ld32(tc0 + 32 * jb, s);
                         const float* w = near + 32 * jb;
                         tc::tmem_ld_wait();
 #pragma unroll
@@ -397,80 +486,98 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         for (int j = 0; j < 16; ++j) r[j] = 0;
                     }
                     // columns 16 jb .. overlay scores of blocks that are read
-                    tc::tmem_st16(ts + 16 * jb, r);
+                    tc::tmem_st16(tc0 + 16 * jb, r);
                 }
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->p_full);
+                if (lane == 0) tc::mbar_arrive(&bars->p_full[c % L::kS]);
             }
             if (!ok) fail();
         }
     } else if (warp < 8) {
-        // ------------------------------------------------ w o K in pieces ----
+        // ------------------------------------- w o K or w o V in pieces ----
+        give();
         const int t = threadIdx.x - 128;
+        const int r = lane & 15, ch = lane >> 4;  // row of a part, first of its 16-byte columns
         bool ok = true;
+        const int part = warp & 1, group0 = (warp - 4) >> 1;  // warps 4, 5: groups 0 and 2 of a chunk
 #pragma unroll 1
         for (int c = 0; ok && c < nch; ++c) {
             const int n = chunk_n(chunk_at(c));
             const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
-            ok = wait_warp(&bars->full[bk.i], bk.use & 1) && (!kOut || wait_warp(&bars->s_full, c & 1));
+            const auto bx = L::kScaleV ? bv : bk;
+            ok = wait_warp(&bars->full[bx.i], bx.use & 1);
+            // k's place is overwritten: by the first piece in the ring, and behind a
+            // partial chunk's end (the scores' columns there are masked, whatever they are)
+            if (kOut && (L::kRing || n < kBlk)) ok = ok && wait_warp(&bars->s_full[c & 1], (c >> 1) & 1);
+            if (n < kBlk) ok = ok && wait_warp(&bars->full[bk.i], bk.use & 1) && wait_warp(&bars->full[bv.i], bv.use & 1);
             if (!ok) break;
             if (n < kBlk) {
-                ok = wait_warp(&bars->full[bv.i], bv.use & 1);
-                if (!ok) break;
-                for (int e = t; e < (kBlk - n) * 8 * (VP / 64); e += 128) {
-                    const int x = e / ((kBlk - n) * 8), f = e - x * (kBlk - n) * 8;
-                    *reinterpret_cast<uint4*>(sm + bv.off + x * kPanel + (n + f / 8) * 128 + (f & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
+                const int each = (kBlk - n) * 8;
+                for (int e = t; e < each * (KP / 64 + VP / 64); e += 128) {
+                    const int x = e / each, f = e - x * each;
+                    const uint32_t off = x < KP / 64 ? bk.off + x * kPanel : bv.off + (x - KP / 64) * kPanel;
+                    // rows of a part belong to its warp where pieces go in place
+                    if (!(L::kRing && x < KP / 64))
+                        *reinterpret_cast<uint4*>(sm + off + (n + f / 8) * 128 + (f & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars->clean);
             }
 #pragma unroll 1
-            for (int u = 0; u < 4; ++u) {
-                const uint32_t qn = 4u * c + u, s = qn & 1;
-                if (qn >= 2) {
-                    ok = wait_warp(&bars->kt_free[s], ((qn >> 1) - 1) & 1);
+            for (int u = group0; u < kGroups; u += 2) {
+                const uint32_t g = (uint32_t)kGroups * c + u, s = g % L::kGroupBufs;
+                if (g >= L::kGroupBufs) {
+                    ok = wait_warp(&bars->x_free[s], (g / L::kGroupBufs - 1) & 1);
                     if (!ok) break;
                 }
-                const int row = 32 * u + lane;
-                const bool in = row < n;
-                const float w = in ? sTab[rev ? row : n - 1 - row] : 0.f;
+                const int row = kPartT * (2 * u + part) + r;
+                const bool inside = row < n;
+                const float w = inside ? sTab[rev ? row : n - 1 - row] : 0.f;
                 const float2 w2 = make_float2(w, w), minus = make_float2(-1.f, -1.f);
-                uint8_t* krow = sm + bk.off + row * 128;
-                uint8_t* prow = sPart + s * (kPieces - 1) * L::kPartB + lane * 128;
+                uint8_t* src = sm + bx.off + row * 128;
+                uint8_t* out = sm + L::OFF_PART + (2 * s + part) * L::kPartB + r * 128;
 #pragma unroll 1
-                for (int x = 0; x < KP / 64; ++x) {
+                for (int x = 0; x < L::kXW / 64; ++x) {
+                    uint4 v[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        // eight neighbouring rows take eight different 16-byte columns
-                        const int cc = ((2 * (warp - 4) + i) ^ (row & 7)) * 16;
-                        const uint4 kv = *reinterpret_cast<const uint4*>(krow + x * kPanel + cc);
-                        const uint32_t in4[4] = {kv.x, kv.y, kv.z, kv.w};
-                        uint32_t o[kPieces][4];
+                    for (int i = 0; i < 4; ++i)  // eight neighbouring rows take eight different 16-byte columns
+                        v[i] = *reinterpret_cast<const uint4*>(src + x * kPanel + ((2 * i + ch) ^ (r & 7)) * 16);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int cc = ((2 * i + ch) ^ (r & 7)) * 16;
+                        if (!inside) v[i] = make_uint4(0, 0, 0, 0);
+                        const uint32_t in4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        uint32_t q[kPieces][4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float2 f = tc::mul2(tc::unpack_bf16x2(in4[e]), w2);
 #pragma unroll
-                            for (int q = 0; q < kPieces; ++q) {
-                                o[q][e] = in ? tc::pack_bf16x2(f.x, f.y) : 0u;
-                                if (q + 1 < kPieces) f = tc::fma2(tc::unpack_bf16x2(o[q][e]), minus, f);
+                            for (int y = 0; y + 1 < kPieces; ++y) {
+                                // the leading 8 bits of each, and what they leave (exactly)
+                                q[y][e] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+                                f = tc::fma2(tc::unpack_bf16x2(q[y][e]), minus, f);
                             }
+                            q[kPieces - 1][e] = tc::pack_bf16x2(f.x, f.y);
                         }
-                        *reinterpret_cast<uint4*>(krow + x * kPanel + cc) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
 #pragma unroll
-                        for (int q = 1; q < kPieces; ++q)
-                            *reinterpret_cast<uint4*>(prow + (q - 1) * L::kPartB + x * kPart + cc) =
-                                make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+                        for (int y = 0; y < kPieces; ++y) {
+                            uint8_t* to = y < L::kFirst ? src + x * kPanel : out + (y - L::kFirst) * L::kPieceB + x * kPartPanel;
+                            *reinterpret_cast<uint4*>(to + cc) = make_uint4(q[y][0], q[y][1], q[y][2], q[y][3]);
+                        }
                     }
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->kt_full[s]);
+                if (lane == 0) tc::mbar_arrive(&bars->x_full[s]);
             }
         }
         if (!ok) fail();
     } else if (warp < 16) {
         // ------------------------------------------------ state and output ----
+        take();
         const int quad = warp & 3, half = (warp - 8) >> 2;
         const int lr = quad * 32 + lane;  // lane of TMEM
         const int c0 = half * CH;
@@ -512,21 +619,19 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             if (lane == 0) tc::mbar_arrive(&bars->h_full);
         };
         if (kOut && nch > 0) put_h();
-        // a backward scan's initial state meets its first token undecayed
-        int off = from_init && rev ? 0 : 1;
-        const float2 whole = decay_power(la, kBlk);
+        int off = off0;
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
             const int t = chunk_at(c), n = chunk_n(t);
-            ok = wait_warp(&bars->z_full, c & 1);
+            ok = wait_warp(&bars->z_full[c % L::kZ], (c / L::kZ) & 1);
             if (!ok) break;
             tc::tc_fence_after();
-            const float2 dec = n - 1 + off == kBlk ? whole : decay_power(la, n - 1 + off);
+            const float2 dec = sDec[c == 0 ? 1 : c + 1 == nch ? 2 : 0];
             const float2 dx = make_float2(dec.x, dec.x), dy = make_float2(dec.y, dec.y);
 #pragma unroll
             for (int x = 0; x < CH / 32; ++x) {
                 float z[32];
-                tc::tmem_ld32(tl + COL_Z + c0 + 32 * x, z);
+                tc::tmem_ld32(tl + L::COL_Z + (c % L::kZ) * 64 + c0 + 32 * x, z);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
@@ -538,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             }
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars->z_free);
+            if (lane == 0) tc::mbar_arrive(&bars->z_free[c % L::kZ]);
             if (kOut) {
                 if (c + 1 < nch) {
                     ok = wait_warp(&bars->h_free, c & 1);  // Q H has read this chunk's H
@@ -548,20 +653,31 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 ok = wait_warp(&bars->o_full, c & 1);
                 if (!ok) break;
                 tc::tc_fence_after();
-                const float e = lr < n ? sTab[(rev ? n - 1 - lr : lr) + off] * R.out_scale : 0.f;
+                const float e = lr < n ? sTab[(rev ? n - 1 - lr : lr) + off] * out_scale : 0.f;
                 const long long row = (long long)it.batch * p.s.plan.T + it.row0 + t + lr;
                 const long long at0 = (row * H + it.head) * V;
                 const bool plain = direct(n);
-                uint8_t* tile = sm + L::buf(c, 1, kOut).off + lr * 128;  // this chunk's K is consumed (z_full)
+                // the ring's tile takes the place of this chunk's V, consumed with z_full and
+                // o_full; the others' is free once the last one has left (waited for in both:
+                // no barrier may get two phases ahead of a warp that waits on it)
+                uint8_t* tile = sm + (L::kRing ? L::buf(c, 2, kOut).off : L::OFF_OUT) + lr * 128;
+                if (c > 0) {
+                    ok = wait_warp(&bars->stored, (c - 1) & 1);
+                    if (!ok) break;
+                }
 #pragma unroll 1
                 for (int x = 0; x < VP / 32; ++x) {
                     const int col = half * (VP / 2) + 16 * x;
                     float a[16], b[16];
-                    tc::tmem_ld16(tl + COL_O1 + col, a);
-                    tc::tmem_ld16(tl + COL_O2 + col, b);
+                    tc::tmem_ld16(tl + L::COL_O1 + col, a);
+                    tc::tmem_ld16(tl + L::COL_O2 + col, b);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) a[q] = fmaf(e, b[q], R.out_scale * a[q]);
+                    for (int q = 0; q < 16; q += 2) {
+                        const float2 y = tc::fma2(make_float2(e, e), make_float2(b[q], b[q + 1]), make_float2(a[q], a[q + 1]));
+                        a[q] = y.x;
+                        a[q + 1] = y.y;
+                    }
                     uint32_t o[8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) o[q] = tc::pack_bf16x2(a[2 * q], a[2 * q + 1]);
@@ -575,9 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         for (int y = 0; y < 2; ++y) {
                             const int cy = col + 8 * y;
                             if (lr >= n || cy >= V ||
-                                !SSD_INB(at0 + cy + 7, (p.s.plan.packed ? 1LL : p.s.plan.B) * p.s.plan.T * H * V))
+                                !SSD_INB(at0 + cy + 7, (packed ? 1LL : p.s.plan.B) * p.s.plan.T * H * V))
                                 continue;
-                            if (R.out_f32) {
+                            if (out_f32) {
                                 float4* f = reinterpret_cast<float4*>((float*)R.out + at0 + cy);
                                 f[0] = make_float4(a[8 * y], a[8 * y + 1], a[8 * y + 2], a[8 * y + 3]);
                                 f[1] = make_float4(a[8 * y + 4], a[8 * y + 5], a[8 * y + 6], a[8 * y + 7]);
@@ -606,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             dst = p.s.states + it.slot * K * V;
         } else if (R.fin && it.seg == it.nseg - 1) {
             dst = R.fin + chain * K * V;
-            mul = R.fin_scale * (rev && it.len > 0 ? decay_power(la, 1).x : 1.f);
+            mul = R.fin_scale * (rev && it.len > 0 ? sTab[1] : 1.f);
         }
         if (ok && dst && holds && SSD_INB(kOut ? chain : it.slot, kOut ? chains : p.s.plan.slots())) {
             dst += (long long)k_of(0) * V + v_of(0);

@@ -239,13 +239,39 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// true in one lane of a converged warp.  Code that the whole warp reaches and one
-// elected lane executes keeps descriptors in uniform registers, where the MMA
-// instructions take them.
-__device__ __forceinline__ bool elect_one() {
+// 1 in one lane of a converged warp, 0 in the others.
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-    return p != 0;
+    return p;
+}
+// mma_ss, mma_ts and mma_commit executed where `e` is non-zero.  A whole warp runs
+// the code around them with e = elect_one(): without a branch on the lane the
+// descriptors stay in uniform registers, where the instructions take them (a
+// product of 16 tokens is issued every 48 cycles at N = 64 and 64 at N = 128;
+// behind a branch on the lane every 74).
+__device__ __forceinline__ void mma_ss_if(uint32_t e, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t e, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(e)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_if(uint32_t e, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(e)
+        : "memory");
 }
 // arrive on an mbarrier once every MMA issued so far by this thread completes
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
