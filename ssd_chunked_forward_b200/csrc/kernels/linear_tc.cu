@@ -22,12 +22,11 @@
 // its rounding would grow with the number of chunks.
 //
 // Warp roles (640 threads):
-//   0-3    scores -> P (thread = row i)
-//   4-7    w o K or w o V in pieces: parts of 16 tokens, each a warp's own (one part
-//          shared by four warps took as long, most of it latency), two parts to a
-//          buffer and a hand-over (one each: the MMA warp spent its time waiting); rows
-//          behind a partial chunk's end become zeros in K and V (with packed
-//          sequences they hold the next sequence's tokens)
+//   0-7    per chunk half of w o K (or w o V) in pieces, scores -> P, the other half:
+//          P by row (lane of TMEM) with two warps for the columns, the pieces by
+//          parts of 16 tokens, two warps to a part, two parts to a buffer and a
+//          hand-over.  Rows behind a partial chunk's end become zeros in K and V
+//          (with packed sequences they hold the next sequence's tokens)
 //   8-15   state and output (two warps per TMEM lane quadrant)
 //   16     TMA loads
 //   17     TMEM; issues S, Q H and P V.  V = 64 leaves TMEM for a second score
@@ -68,6 +67,16 @@ struct __align__(8) Bars {
     uint64_t done, z_done;
 };
 
+// Matrix descriptors (128-byte swizzle, 1024 bytes from one group of eight rows to
+// the next) by their low words: start address and leading-dimension offset.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+    return ((saddr >> 4) & 0x3FFF) | (lbo_bytes >> 4) << 16;
+}
+__device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t adv_bytes) {
+    constexpr uint32_t hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+    return (uint64_t)hi << 32 | (lo + (adv_bytes >> 4));
+}
+
 struct TcParams {
     CUtensorMap map[kScanRoles][4];  // q, k, v, out
     ScanLaunch s;
@@ -104,7 +113,7 @@ struct Layout {
     static_assert(kBytes <= 232448, "shared memory above the 227 KB per-block limit");
     static_assert(OFF_PART % 1024 == 0 && OFF_H % 1024 == 0 && OFF_OUT % 1024 == 0, "swizzled tiles start on 1024 bytes");
 
-    // TMEM columns: scores (P in their first 64), P V, Q H, Z
+    // TMEM columns: scores (P in 0-31 and 64-95 of them), P V, Q H, Z
     static constexpr int kS = VP == 64 ? 2 : 1;
     static constexpr int kZ = VP == 64 ? 2 : 1;
     static constexpr uint32_t COL_S = 0, COL_O1 = 128 * kS, COL_O2 = COL_O1 + VP, COL_Z = 384;
@@ -193,15 +202,15 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars->s_full[i], 1);
-            tc::mbar_init(&bars->p_full[i], 4);
+            tc::mbar_init(&bars->p_full[i], 8);
         }
         tc::mbar_init(&bars->o_full, 1);
         tc::mbar_init(&bars->o_free, 8);
         for (int i = 0; i < kMaxGroupBufs; ++i) {
-            tc::mbar_init(&bars->x_full[i], 2);
+            tc::mbar_init(&bars->x_full[i], 4);
             tc::mbar_init(&bars->x_free[i], 1);
         }
-        tc::mbar_init(&bars->clean, 4);
+        tc::mbar_init(&bars->clean, 8);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars->z_full[i], 1);
             tc::mbar_init(&bars->z_free[i], 8);
@@ -251,7 +260,6 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, wait_here(bar, parity, abort_v));
     };
-    // first token (in the sequence) and tokens of the c-th chunk in scan order
     // Arrivals on a tile's empty barrier once the products issued so far are done.
     // Buffers of the ring hold q, k and v in turn and expect three arrivals each
     // time: Q H makes q's three, S one and Z two of k's, P V, Z and the output's
@@ -261,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         if (kOut && L::kRing)
             for (int i = 1; i < in_ring; ++i) tc::mma_commit_if(e, &bars->empty[buf]);
     };
+    // first token (in the sequence) and tokens of the c-th chunk in scan order
     auto chunk_at = [&](int c) -> int { return it.t0 + (rev ? nch - 1 - c : c) * kBlk; };
     auto chunk_n = [&](int t) -> int { return min(kBlk, it.t1 - t); };
     // a chunk of n tokens whose output leaves by plain stores: fp32, or a packed
@@ -304,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         const uint32_t base = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const int chunks = __shfl_sync(0xffffffffu, nch, 0);
-        const uint64_t kmaj = tc::smem_desc_sw128(base, 16, 1024);       // rows contiguous along the contraction
-        const uint64_t mnmaj = tc::smem_desc_sw128(base, kPanel, 1024);  // contraction along the rows
+        const uint32_t kmaj = desc_lo(base, 16);       // rows contiguous along the contraction
+        const uint32_t mnmaj = desc_lo(base, kPanel);  // contraction along the rows
         const uint32_t lead = tc::elect_one();
         bool ok = true;
         // S of chunk c
@@ -316,12 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             if (c >= L::kS && !wait_warp(&bars->o_full, (c - L::kS) & 1)) return false;
             tc::tc_fence_after();
             {
-                const uint64_t dq = tc::desc_adv(kmaj, bq.off), dk = tc::desc_adv(kmaj, bk.off);
+                const uint32_t dq = kmaj + (bq.off >> 4), dk = kmaj + (bk.off >> 4);
                 const uint32_t d = tm + L::COL_S + (c % L::kS) * 128;
 #pragma unroll
                 for (int kk = 0; kk < KP / 16; ++kk) {
                     const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                    tc::mma_ss_if(lead, d, tc::desc_adv(dq, off), tc::desc_adv(dk, off), id_s, kk > 0);
+                    tc::mma_ss_if(lead, d, desc(dq, off), desc(dk, off), id_s, kk > 0);
                 }
                 tc::mma_commit_if(lead, &bars->s_full[c & 1]);
                 release(lead, bk.i, 1);
@@ -340,12 +349,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             const auto bv = L::buf(c, 2, kOut);
             {
                 const auto bq = L::buf(c, 0, kOut);
-                const uint64_t dq = tc::desc_adv(kmaj, bq.off);
+                const uint32_t dq = kmaj + ((bq.off) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < KP / 16; ++kk) {
                     const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                    const uint64_t dh = kLaneV ? tc::desc_adv(kmaj, L::OFF_H + off) : tc::desc_adv(mnmaj, L::OFF_H + kk * 2048);
-                    tc::mma_ss_if(lead, tm + L::COL_O2, tc::desc_adv(dq, off), dh, id_qh, kk > 0);
+                    const uint64_t dh = kLaneV ? desc(kmaj, L::OFF_H + off) : desc(mnmaj, L::OFF_H + kk * 2048);
+                    tc::mma_ss_if(lead, tm + L::COL_O2, desc(dq, off), dh, id_qh, kk > 0);
                 }
                 tc::mma_commit_if(lead, &bars->h_free);
                 release(lead, bq.i, 3);
@@ -356,11 +365,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             if (!ok) break;
             tc::tc_fence_after();
             {
-                const uint64_t dv = tc::desc_adv(mnmaj, bv.off);
+                const uint32_t dv = mnmaj + ((bv.off) >> 4);
                 const uint32_t a = tm + L::COL_S + (c % L::kS) * 128;
 #pragma unroll
                 for (int kk = 0; kk < kBlk / 16; ++kk)
-                    tc::mma_ts_if(lead, tm + L::COL_O1, a + kk * 8, tc::desc_adv(dv, kk * 2048), id_pv, kk > 0);
+                    tc::mma_ts_if(lead, tm + L::COL_O1, a + (kk >> 2) * 64 + (kk & 3) * 8, desc(dv, kk * 2048), id_pv, kk > 0);
                 tc::mma_commit_if(lead, &bars->o_full);
                 release(lead, bv.i, 1);
             }
@@ -375,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         const uint32_t base = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const int chunks = __shfl_sync(0xffffffffu, nch, 0);
-        const uint64_t mnmaj = tc::smem_desc_sw128(base, kPanel, 1024);
-        const uint64_t partmn = tc::smem_desc_sw128(base + L::OFF_PART, kPartPanel, 1024);
+        const uint32_t mnmaj = desc_lo(base, kPanel);
+        const uint32_t partmn = desc_lo(base + L::OFF_PART, kPartPanel);
         const uint32_t lead = tc::elect_one();
         bool ok = true;
 #pragma unroll 1
@@ -388,24 +397,24 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             if (!ok) break;
             tc::tc_fence_after();
             // the operand that stays whole fills the MMA's rows
-            const uint64_t whole = tc::desc_adv(mnmaj, L::kScaleV ? bk.off : bv.off);
-            const uint64_t inplace = tc::desc_adv(mnmaj, bk.off);
+            const uint32_t whole = mnmaj + ((L::kScaleV ? bk.off : bv.off) >> 4);
+            const uint32_t inplace = mnmaj + ((bk.off) >> 4);
             const uint32_t z = tm + L::COL_Z + (c % L::kZ) * 64;
 #pragma unroll 1
             for (int u = 0; u < kGroups; ++u) {
                 const uint32_t g = (uint32_t)kGroups * c + u, s = g % L::kGroupBufs;
                 ok = wait_warp(&bars->x_full[s], (g / L::kGroupBufs) & 1);
                 if (!ok) break;
-                const uint64_t da = tc::desc_adv(whole, u * 2 * kPartPanel);
-                const uint64_t di = tc::desc_adv(inplace, u * 2 * kPartPanel);
-                const uint64_t dx = tc::desc_adv(partmn, s * 2 * L::kPartB);
+                const uint32_t da = whole + ((u * 2 * kPartPanel) >> 4);
+                const uint32_t di = inplace + ((u * 2 * kPartPanel) >> 4);
+                const uint32_t dx = partmn + ((s * 2 * L::kPartB) >> 4);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int x = 0; x < kPieces; ++x)
-                        tc::mma_ss_if(lead, z, tc::desc_adv(da, i * kPartPanel),
-                                      x < L::kFirst ? tc::desc_adv(di, i * kPartPanel)
-                                                    : tc::desc_adv(dx, i * L::kPartB + (x - L::kFirst) * L::kPieceB),
+                        tc::mma_ss_if(lead, z, desc(da, i * kPartPanel),
+                                      x < L::kFirst ? desc(di, i * kPartPanel)
+                                                    : desc(dx, i * L::kPartB + (x - L::kFirst) * L::kPieceB),
                                       id_z, (u > 0 || i > 0 || x > 0) ? 1u : 0u);
                 tc::mma_commit_if(lead, &bars->x_free[s]);
             }
@@ -440,68 +449,18 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             }
             if (!ok) fail();
         }
-    } else if (warp < 4) {
-        give();
-        if (kOut) {
-            // ------------------------------------- P = S o L, thread = row ----
-            const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16) + L::COL_S;
-            // out_scale l^|i-j| of row i against the columns of block jb: 32 consecutive
-            // entries of a table, neighbouring lanes one apart
-            const float* near = sNear + (rev ? 32 : kBlk - 1) - (32 * warp + lane);
-            const uint32_t diag = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
-            bool ok = true;
-#pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
-                const int n = chunk_n(chunk_at(c));
-                const uint32_t tc0 = ts + (c % L::kS) * 128;
-                ok = wait_warp(&bars->s_full[c & 1], (c >> 1) & 1);
-                if (!ok) break;
-                tc::tc_fence_after();
-#pragma unroll 1
-                for (int jb = 0; jb < 4; ++jb) {
-                    // the block's columns on the causal side and in the chunk
-                    uint32_t m = jb == warp ? diag : (rev ? jb > warp : jb < warp) ? 0xffffffffu : 0u;
-                    if (n < 32 * jb + 32) m &= n > 32 * jb ? 0xffffffffu >> (32 * jb + 32 - n) : 0u;
-                    uint32_t r[16];
-                    if (__any_sync(0xffffffffu, m != 0)) {
-                        float s[32];
-                        tc::tmem_ld32(tc0 + 32 * jb, s);
-                        const float* w = near + 32 * jb;
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 v = tc::mul2(make_float2(s[2 * j], s[2 * j + 1]), make_float2(w[2 * j], w[2 * j + 1]));
-                            s[2 * j] = v.x;
-                            s[2 * j + 1] = v.y;
-                        }
-                        // a product with 0 would keep a NaN of a masked place
-                        if (!__all_sync(0xffffffffu, m == 0xffffffffu)) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) s[j] = (m >> j) & 1 ? s[j] : 0.f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) r[j] = tc::pack_bf16x2(s[2 * j], s[2 * j + 1]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) r[j] = 0;
-                    }
-                    // columns 16 jb .. overlay scores of blocks that are read
-                    tc::tmem_st16(tc0 + 16 * jb, r);
-                }
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->p_full[c % L::kS]);
-            }
-            if (!ok) fail();
-        }
     } else if (warp < 8) {
-        // ------------------------------------- w o K or w o V in pieces ----
+        // --------------------------------- pieces of w o K or w o V, and P ----
         give();
-        const int t = threadIdx.x - 128;
-        const int r = lane & 15, ch = lane >> 4;  // row of a part, first of its 16-byte columns
+        const int quad = warp & 3, half = warp >> 2;  // rows and columns of P
+        const uint32_t ts = tmem + ((uint32_t)(quad * 32) << 16) + L::COL_S;
+        // out_scale l^|i-j| of row i against the columns of block jb: 32 consecutive
+        // entries of a table, neighbouring lanes one apart
+        const float* near = sNear + (rev ? 32 : kBlk - 1) - (32 * quad + lane);
+        const uint32_t diag = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+        // this warp's part among the four of half a chunk, row of it, 16-byte column
+        const int part = warp >> 1, r = (lane & 7) + 8 * (warp & 1), ch = lane >> 3;
         bool ok = true;
-        const int part = warp & 1, group0 = (warp - 4) >> 1;  // warps 4, 5: groups 0 and 2 of a chunk
 #pragma unroll 1
         for (int c = 0; ok && c < nch; ++c) {
             const int n = chunk_n(chunk_at(c));
@@ -515,10 +474,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             if (!ok) break;
             if (n < kBlk) {
                 const int each = (kBlk - n) * 8;
-                for (int e = t; e < each * (KP / 64 + VP / 64); e += 128) {
+                for (int e = threadIdx.x; e < each * (KP / 64 + VP / 64); e += 256) {
                     const int x = e / each, f = e - x * each;
                     const uint32_t off = x < KP / 64 ? bk.off + x * kPanel : bv.off + (x - KP / 64) * kPanel;
-                    // rows of a part belong to its warp where pieces go in place
+                    // where pieces go in place, the rows belong to their part's warps
                     if (!(L::kRing && x < KP / 64))
                         *reinterpret_cast<uint4*>(sm + off + (n + f / 8) * 128 + (f & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
@@ -527,29 +486,28 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 if (lane == 0) tc::mbar_arrive(&bars->clean);
             }
 #pragma unroll 1
-            for (int u = group0; u < kGroups; u += 2) {
+            for (int hc = 0; hc < 2; ++hc) {
+                const int u = 2 * hc + (part >> 1);  // group of the chunk
                 const uint32_t g = (uint32_t)kGroups * c + u, s = g % L::kGroupBufs;
                 if (g >= L::kGroupBufs) {
                     ok = wait_warp(&bars->x_free[s], (g / L::kGroupBufs - 1) & 1);
                     if (!ok) break;
                 }
-                const int row = kPartT * (2 * u + part) + r;
+                const int row = 64 * hc + kPartT * part + r;
                 const bool inside = row < n;
                 const float w = inside ? sTab[rev ? row : n - 1 - row] : 0.f;
                 const float2 w2 = make_float2(w, w), minus = make_float2(-1.f, -1.f);
                 uint8_t* src = sm + bx.off + row * 128;
-                uint8_t* out = sm + L::OFF_PART + (2 * s + part) * L::kPartB + r * 128;
-#pragma unroll 1
+                uint8_t* out = sm + L::OFF_PART + (2 * s + (part & 1)) * L::kPartB + r * 128;
+#pragma unroll
                 for (int x = 0; x < L::kXW / 64; ++x) {
-                    uint4 v[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)  // eight neighbouring rows take eight different 16-byte columns
-                        v[i] = *reinterpret_cast<const uint4*>(src + x * kPanel + ((2 * i + ch) ^ (r & 7)) * 16);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int cc = ((2 * i + ch) ^ (r & 7)) * 16;
-                        if (!inside) v[i] = make_uint4(0, 0, 0, 0);
-                        const uint32_t in4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    for (int i = 0; i < 2; ++i) {
+                        // eight neighbouring rows take eight different 16-byte columns
+                        const int cc = ((4 * i + ch) ^ (r & 7)) * 16;
+                        uint4 v = *reinterpret_cast<const uint4*>(src + x * kPanel + cc);
+                        if (!inside) v = make_uint4(0, 0, 0, 0);
+                        const uint32_t in4[4] = {v.x, v.y, v.z, v.w};
                         uint32_t q[kPieces][4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -558,7 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                             for (int y = 0; y + 1 < kPieces; ++y) {
                                 // the leading 8 bits of each, and what they leave (exactly)
                                 q[y][e] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-                                f = tc::fma2(tc::unpack_bf16x2(q[y][e]), minus, f);
+                                f = tc::fma2(make_float2(__uint_as_float(__float_as_uint(f.x) & 0xffff0000u),
+                                                         __uint_as_float(__float_as_uint(f.y) & 0xffff0000u)), minus, f);
                             }
                             q[kPieces - 1][e] = tc::pack_bf16x2(f.x, f.y);
                         }
@@ -572,6 +531,46 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars->x_full[s]);
+                if (!kOut || hc == 1) continue;
+                const uint32_t tc0 = ts + (c % L::kS) * 128;
+                ok = wait_warp(&bars->s_full[c & 1], (c >> 1) & 1);
+                if (!ok) break;
+                tc::tc_fence_after();
+#pragma unroll 1
+                for (int jb = 2 * half; jb < 2 * half + 2; ++jb) {
+                    // the block's columns on the causal side and in the chunk
+                    uint32_t m = jb == quad ? diag : (rev ? jb > quad : jb < quad) ? 0xffffffffu : 0u;
+                    if (n < 32 * jb + 32) m &= n > 32 * jb ? 0xffffffffu >> (32 * jb + 32 - n) : 0u;
+                    uint32_t pr[16];
+                    if (__any_sync(0xffffffffu, m != 0)) {
+                        float sc[32];
+                        tc::tmem_ld32(tc0 + 32 * jb, sc);
+                        const float* wl = near + 32 * jb;
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 y = tc::mul2(make_float2(sc[2 * j], sc[2 * j + 1]), make_float2(wl[2 * j], wl[2 * j + 1]));
+                            sc[2 * j] = y.x;
+                            sc[2 * j + 1] = y.y;
+                        }
+                        // a product with 0 would keep a NaN of a masked place
+                        if (!__all_sync(0xffffffffu, m == 0xffffffffu)) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sc[j] = (m >> j) & 1 ? sc[j] : 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) pr[j] = tc::pack_bf16x2(sc[2 * j], sc[2 * j + 1]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) pr[j] = 0;
+                    }
+                    // each half's P overlays scores of its own that are read
+                    tc::tmem_st16(tc0 + 64 * half + 16 * (jb & 1), pr);
+                }
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars->p_full[c % L::kS]);
             }
         }
         if (!ok) fail();
