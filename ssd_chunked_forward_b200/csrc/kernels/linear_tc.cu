@@ -22,21 +22,20 @@
 // its rounding would grow with the number of chunks.
 //
 // Warp roles (640 threads):
-//   0-7    per chunk half of w o K (or w o V) in pieces, scores -> P, the other half:
-//          P by row (lane of TMEM) with two warps for the columns, the pieces by
-//          parts of 16 tokens, two warps to a part, two parts to a buffer and a
-//          hand-over.  Rows behind a partial chunk's end become zeros in K and V
-//          (with packed sequences they hold the next sequence's tokens)
-//   8-15   state and output (two warps per TMEM lane quadrant)
-//   16     TMA loads
-//   17     TMEM; issues S, Q H and P V.  V = 64 leaves TMEM for a second score
-//          buffer: the next chunk's S goes first, so that P is made a chunk ahead
-//   18     TMA stores of output tiles (plain stores of rows by their threads touch
-//          32 lines each: they kept the load/store unit busy for 2000 cycles a chunk)
-//   19     issues Z.  An MMA of 128 rows and 16 tokens takes 43 + N / 2 cycles with
-//          both operands in shared memory, 10 + N / 2 with P in TMEM (measured): a
-//          chunk's products are 3600 cycles at K = 128, V = 64, 4900 at 128, 128, with
-//          the loads' share of HBM at 4100 and 5500.
+//   0-3    scores -> P (thread = row i)
+//   4-7    w o K or w o V in pieces: parts of 16 tokens, each a warp's own, two parts
+//          to a buffer and a hand-over; rows behind a partial chunk's end become
+//          zeros in K and V (with packed sequences they hold the next one's tokens)
+//   8-15   state and output, two warps to a TMEM lane quadrant
+//   16     lane 0 loads tiles by TMA; lane 1 stores output tiles (plain stores of rows
+//          by their threads touch 32 lines each and kept the load/store unit busy
+//          for 2000 cycles a chunk)
+//   17     TMEM; issues Q H and P V
+//   18     issues S, a chunk ahead where V = 64 leaves TMEM for a second score buffer
+//   19     issues Z.  An MMA of 128 rows and 16 tokens takes 48 cycles at N = 64 and 64
+//          at N = 128 (measured): a chunk's products are 2700 cycles at K = 128, V =
+//          64 and 3100 at 128, 128; its loads and stores at the card's copy rate
+//          are 4100 and 5500.
 //
 // With V = 128 the lanes of Z are the state's columns (v), else its rows (k): an
 // MMA takes 128 rows, and the other order would waste half of them.
@@ -51,6 +50,8 @@ namespace {
 
 constexpr int kBlk = kScanChunk;         // 128 tokens: the MMA's M
 constexpr int kThreads = 640;
+constexpr int kState = 8, kStateWarps = 8;  // first warp of the state's, how many
+constexpr int kLoads = 16, kOutputs = 17, kScores = 18, kStates = 19;
 constexpr uint32_t kPanel = kBlk * 128;  // 128 rows of 64 bf16
 constexpr int kPartT = 16;               // tokens of a part: the MMA's K
 constexpr uint32_t kPartPanel = kPartT * 128;
@@ -61,10 +62,10 @@ struct __align__(8) Bars {
     uint64_t full[kMaxBufs], empty[kMaxBufs];
     // s_full alternates even with one score buffer: the next chunk's S may be done
     // before the warps that make the pieces have seen this one's
-    uint64_t s_full[2], p_full[2], o_full, o_free;
+    uint64_t s_full[2], s_free[2], p_full[2], o_full, o_free;
     uint64_t x_full[kMaxGroupBufs], x_free[kMaxGroupBufs], clean;
     uint64_t z_full[2], z_free[2], h_full, h_free, staged, stored;
-    uint64_t done, z_done;
+    uint64_t done, z_done, s_done;
 };
 
 // Matrix descriptors (128-byte swizzle, 1024 bytes from one group of eight rows to
@@ -113,7 +114,7 @@ struct Layout {
     static_assert(kBytes <= 232448, "shared memory above the 227 KB per-block limit");
     static_assert(OFF_PART % 1024 == 0 && OFF_H % 1024 == 0 && OFF_OUT % 1024 == 0, "swizzled tiles start on 1024 bytes");
 
-    // TMEM columns: scores (P in 0-31 and 64-95 of them), P V, Q H, Z
+    // TMEM columns: scores (P in their first 64), P V, Q H, Z
     static constexpr int kS = VP == 64 ? 2 : 1;
     static constexpr int kZ = VP == 64 ? 2 : 1;
     static constexpr uint32_t COL_S = 0, COL_O1 = 128 * kS, COL_O2 = COL_O1 + VP, COL_Z = 384;
@@ -138,15 +139,28 @@ struct Layout {
     }
 };
 
-// The bounded wait of tc_common.cuh without its out-of-line part: a call would
-// spill the state that the warps hold in registers.
-__device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity, const volatile int* abort) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = tc::globaltimer_ns();
-    for (;;) {
-        if (tc::mbar_try_wait_sleep(bar, parity, 500000u)) return true;
-        if (*abort || tc::globaltimer_ns() - t0 > 2000000000ull) return false;
-    }
+// A bounded wait in few instructions (each role's loop is executed once per chunk,
+// and all of them together have to stay in the instruction cache; a call would
+// spill the state that the warps hold in registers).  A try sleeps up to a
+// microsecond; the longest wait of a healthy run is some tens of them, and after
+// 2^20 tries (25 ms at the very least, a second as a rule) the wait has failed.
+__device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 1048576;\n"
+        "WAIT_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "@p bra DONE_%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra WAIT_%=;\n"
+        "DONE_%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 template <int KP, int VP, bool kOut, int kPieces>
@@ -164,9 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     float2* sDec = reinterpret_cast<float2*>(sm + L::OFF_DEC);
     Bars* bars = reinterpret_cast<Bars*>(sm + L::OFF_BAR);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::OFF_MISC);
-    int* sAbort = reinterpret_cast<int*>(sm + L::OFF_MISC + 4);
     ScanItem* sItem = reinterpret_cast<ScanItem*>(sm + L::OFF_ITEM);
-    volatile int* abort_v = sAbort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (p.s.reset && blockIdx.x == 0 && threadIdx.x == 0) *p.s.status = kDevOk;
@@ -193,38 +205,37 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
 
     if (threadIdx.x == 32) {
         for (int i = 0; i < L::kBufs; ++i) {
-            // a tile's place is free again when each of its products is done (q: Q H
-            // after S; k: S, Z; v: P V, Z) and, in the ring, v's output has left
-            int users = 1;
-            if (kOut && !L::kRing) users = i % 3 == 0 ? 1 : 2;
+            // a tile's place is free again when both its products are done (q: S, Q H;
+            // k: S, Z; v: P V, Z) and, in the ring, v's output has left
             tc::mbar_init(&bars->full[i], 1);
-            tc::mbar_init(&bars->empty[i], kOut && L::kRing ? 3 : users);
+            tc::mbar_init(&bars->empty[i], !kOut ? 1 : L::kRing ? 3 : 2);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars->s_full[i], 1);
-            tc::mbar_init(&bars->p_full[i], 8);
+            tc::mbar_init(&bars->s_free[i], 1);
+            tc::mbar_init(&bars->p_full[i], 4);
         }
         tc::mbar_init(&bars->o_full, 1);
-        tc::mbar_init(&bars->o_free, 8);
+        tc::mbar_init(&bars->o_free, kStateWarps);
         for (int i = 0; i < kMaxGroupBufs; ++i) {
-            tc::mbar_init(&bars->x_full[i], 4);
+            tc::mbar_init(&bars->x_full[i], 2);
             tc::mbar_init(&bars->x_free[i], 1);
         }
-        tc::mbar_init(&bars->clean, 8);
+        tc::mbar_init(&bars->clean, 4);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars->z_full[i], 1);
-            tc::mbar_init(&bars->z_free[i], 8);
+            tc::mbar_init(&bars->z_free[i], kStateWarps);
         }
-        tc::mbar_init(&bars->h_full, 8);
+        tc::mbar_init(&bars->h_full, kStateWarps);
         tc::mbar_init(&bars->h_free, 1);
-        tc::mbar_init(&bars->staged, 8);
+        tc::mbar_init(&bars->staged, kStateWarps);
         tc::mbar_init(&bars->stored, 1);
         tc::mbar_init(&bars->z_done, 1);
+        tc::mbar_init(&bars->s_done, 1);
         tc::mbar_init(&bars->done, 1);
-        *sAbort = 0;
         tc::fence_mbar_init();
     }
-    if (warp == 17) {
+    if (warp == kOutputs) {
         tc::tmem_alloc(sTmem, 512);
         tc::tmem_relinquish();
     }
@@ -251,23 +262,19 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     auto give = [] { if constexpr (CH == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); };
     auto take = [] { if constexpr (CH == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 120;"); };
 
-    auto fail = [&]() {
-        *reinterpret_cast<volatile int*>(sAbort) = 1;
-        atomicExch(p.s.status, kDevTimeout);
-    };
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_here(bar, parity, abort_v); };
+    auto fail = [&]() { atomicExch(p.s.status, kDevTimeout); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_here(bar, parity); };
     // the same decision in every lane: what follows is executed by whole warps
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait_here(bar, parity, abort_v));
+        return __all_sync(0xffffffffu, wait_here(bar, parity));
     };
-    // Arrivals on a tile's empty barrier once the products issued so far are done.
-    // Buffers of the ring hold q, k and v in turn and expect three arrivals each
-    // time: Q H makes q's three, S one and Z two of k's, P V, Z and the output's
-    // store one each of v's.
+    // Arrivals on a tile's empty barrier once the products that this thread issued so
+    // far are done.  Buffers of the ring hold q, k and v in turn and expect three
+    // arrivals each time: S makes one of q's and k's, Q H and Z the other two, P V, Z
+    // and the output's store one each of v's.
     auto release = [&](uint32_t e, uint32_t buf, int in_ring) {
         tc::mma_commit_if(e, &bars->empty[buf]);
-        if (kOut && L::kRing)
-            for (int i = 1; i < in_ring; ++i) tc::mma_commit_if(e, &bars->empty[buf]);
+        if (kOut && L::kRing && in_ring == 2) tc::mma_commit_if(e, &bars->empty[buf]);
     };
     // first token (in the sequence) and tokens of the c-th chunk in scan order
     auto chunk_at = [&](int c) -> int { return it.t0 + (rev ? nch - 1 - c : c) * kBlk; };
@@ -276,23 +283,26 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     // sequence's end, behind which the rows are another's
     auto direct = [&](int n) -> bool { return out_f32 || (packed && n < kBlk); };
 
-    if (warp == 16) {
+    if (warp == kLoads) {
         if (lane == 0) {
             // ------------------------------------------------- TMA loads ----
             bool ok = true;
-            const int head[3] = {it.head / R.q.share, it.head / R.k.share, it.head / R.v.share};
+            const int hq = it.head / R.q.share;
+            const int hk = it.head / R.k.share, hv = it.head / R.v.share;
             int c = 0;
+#pragma unroll 1
             for (; ok && c < nch; ++c) {
                 const int row = (int)(it.row0 + chunk_at(c));
-#pragma unroll
+#pragma unroll 1
                 for (int w = kOut ? 0 : 1; w < 3; ++w) {
                     const auto b = L::buf(c, w, kOut);
                     if (b.use > 0 && !wait(&bars->empty[b.i], (b.use - 1) & 1)) { ok = false; break; }
                     const int panels = (w == 2 ? VP : KP) / 64;
                     tc::mbar_arrive_expect_tx(&bars->full[b.i], panels * kPanel);
+#pragma unroll 1
                     for (int x = 0; x < panels; ++x)
                         tc::tma_load_4d(sm + b.off + x * kPanel, &p.map[it.role][w], &bars->full[b.i], 64 * x,
-                                        head[w], row, it.batch);
+                                        w == 0 ? hq : w == 1 ? hk : hv, row, it.batch);
                 }
             }
             if (!ok) {
@@ -304,130 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         tc::mbar_wait(&bars->full[b.i], b.use & 1, nullptr, 200000000ull);
                     }
             }
-        }
-    } else if (warp == 17) {
-        // ----------------------------------------------------- MMA issue ----
-        constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);
-        constexpr uint32_t id_pv = tc::idesc_bf16_f32(128, VP, 0, 1);
-        constexpr uint32_t id_qh = tc::idesc_bf16_f32(128, VP, 0, kLaneV ? 0 : 1);
-        const uint32_t base = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const int chunks = __shfl_sync(0xffffffffu, nch, 0);
-        const uint32_t kmaj = desc_lo(base, 16);       // rows contiguous along the contraction
-        const uint32_t mnmaj = desc_lo(base, kPanel);  // contraction along the rows
-        const uint32_t lead = tc::elect_one();
-        bool ok = true;
-        // S of chunk c
-        auto scores = [&](int c) -> bool {
-            const auto bq = L::buf(c, 0, kOut), bk = L::buf(c, 1, kOut);
-            if (!(wait_warp(&bars->full[bq.i], bq.use & 1) && wait_warp(&bars->full[bk.i], bk.use & 1))) return false;
-            // they overwrite the P that P V of the chunk kS before read
-            if (c >= L::kS && !wait_warp(&bars->o_full, (c - L::kS) & 1)) return false;
-            tc::tc_fence_after();
-            {
-                const uint32_t dq = kmaj + (bq.off >> 4), dk = kmaj + (bk.off >> 4);
-                const uint32_t d = tm + L::COL_S + (c % L::kS) * 128;
-#pragma unroll
-                for (int kk = 0; kk < KP / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                    tc::mma_ss_if(lead, d, desc(dq, off), desc(dk, off), id_s, kk > 0);
-                }
-                tc::mma_commit_if(lead, &bars->s_full[c & 1]);
-                release(lead, bk.i, 1);
-            }
-            return true;
-        };
-        if (kOut && L::kS == 2 && chunks > 0) ok = scores(0);
-#pragma unroll 1
-        for (int c = 0; kOut && ok && c < chunks; ++c) {
-            if (L::kS == 1) ok = scores(c);
-            else if (c + 1 < chunks) ok = scores(c + 1);
-            // Q H
-            ok = ok && wait_warp(&bars->h_full, c & 1) && (c == 0 || wait_warp(&bars->o_free, (c - 1) & 1));
-            if (!ok) break;
-            tc::tc_fence_after();
-            const auto bv = L::buf(c, 2, kOut);
-            {
-                const auto bq = L::buf(c, 0, kOut);
-                const uint32_t dq = kmaj + ((bq.off) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < KP / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                    const uint64_t dh = kLaneV ? desc(kmaj, L::OFF_H + off) : desc(mnmaj, L::OFF_H + kk * 2048);
-                    tc::mma_ss_if(lead, tm + L::COL_O2, desc(dq, off), dh, id_qh, kk > 0);
-                }
-                tc::mma_commit_if(lead, &bars->h_free);
-                release(lead, bq.i, 3);
-            }
-            // P V
-            ok = wait_warp(&bars->full[bv.i], bv.use & 1) && wait_warp(&bars->p_full[c % L::kS], (c / L::kS) & 1) &&
-                 (chunk_n(chunk_at(c)) == kBlk || wait_warp(&bars->clean, 0));
-            if (!ok) break;
-            tc::tc_fence_after();
-            {
-                const uint32_t dv = mnmaj + ((bv.off) >> 4);
-                const uint32_t a = tm + L::COL_S + (c % L::kS) * 128;
-#pragma unroll
-                for (int kk = 0; kk < kBlk / 16; ++kk)
-                    tc::mma_ts_if(lead, tm + L::COL_O1, a + (kk >> 2) * 64 + (kk & 3) * 8, desc(dv, kk * 2048), id_pv, kk > 0);
-                tc::mma_commit_if(lead, &bars->o_full);
-                release(lead, bv.i, 1);
-            }
-        }
-        if (!ok) fail();
-        // every product issued must be complete before TMEM is released
-        tc::mma_commit_if(lead, &bars->done);
-        tc::mbar_wait(&bars->done, 0, nullptr, 200000000ull);
-    } else if (warp == 19) {
-        // ------------------------------------------------- Z = (w o K)^T V ----
-        constexpr uint32_t id_z = tc::idesc_bf16_f32(128, L::kXW, 1, 1);
-        const uint32_t base = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const int chunks = __shfl_sync(0xffffffffu, nch, 0);
-        const uint32_t mnmaj = desc_lo(base, kPanel);
-        const uint32_t partmn = desc_lo(base + L::OFF_PART, kPartPanel);
-        const uint32_t lead = tc::elect_one();
-        bool ok = true;
-#pragma unroll 1
-        for (int c = 0; ok && c < chunks; ++c) {
-            const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
-            ok = wait_warp(&bars->full[bk.i], bk.use & 1) && wait_warp(&bars->full[bv.i], bv.use & 1) &&
-                 (c < L::kZ || wait_warp(&bars->z_free[c % L::kZ], (c / L::kZ - 1) & 1)) &&
-                 (chunk_n(chunk_at(c)) == kBlk || wait_warp(&bars->clean, 0));
-            if (!ok) break;
-            tc::tc_fence_after();
-            // the operand that stays whole fills the MMA's rows
-            const uint32_t whole = mnmaj + ((L::kScaleV ? bk.off : bv.off) >> 4);
-            const uint32_t inplace = mnmaj + ((bk.off) >> 4);
-            const uint32_t z = tm + L::COL_Z + (c % L::kZ) * 64;
-#pragma unroll 1
-            for (int u = 0; u < kGroups; ++u) {
-                const uint32_t g = (uint32_t)kGroups * c + u, s = g % L::kGroupBufs;
-                ok = wait_warp(&bars->x_full[s], (g / L::kGroupBufs) & 1);
-                if (!ok) break;
-                const uint32_t da = whole + ((u * 2 * kPartPanel) >> 4);
-                const uint32_t di = inplace + ((u * 2 * kPartPanel) >> 4);
-                const uint32_t dx = partmn + ((s * 2 * L::kPartB) >> 4);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int x = 0; x < kPieces; ++x)
-                        tc::mma_ss_if(lead, z, desc(da, i * kPartPanel),
-                                      x < L::kFirst ? desc(di, i * kPartPanel)
-                                                    : desc(dx, i * L::kPartB + (x - L::kFirst) * L::kPieceB),
-                                      id_z, (u > 0 || i > 0 || x > 0) ? 1u : 0u);
-                tc::mma_commit_if(lead, &bars->x_free[s]);
-            }
-            if (!ok) break;
-            tc::mma_commit_if(lead, &bars->z_full[c % L::kZ]);
-            release(lead, bk.i, 2);
-            release(lead, bv.i, 1);
-        }
-        if (!ok) fail();
-        tc::mma_commit_if(lead, &bars->z_done);
-        tc::mbar_wait(&bars->z_done, 0, nullptr, 200000000ull);
-    } else if (warp == 18) {
-        if (kOut && lane == 0) {
+        } else if (kOut && lane == 1) {
             // ---------------------------------------------------- TMA stores ----
             bool ok = true;
             for (int c = 0; c < nch; ++c) {
@@ -449,18 +336,177 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             }
             if (!ok) fail();
         }
-    } else if (warp < 8) {
-        // --------------------------------- pieces of w o K or w o V, and P ----
-        give();
-        const int quad = warp & 3, half = warp >> 2;  // rows and columns of P
-        const uint32_t ts = tmem + ((uint32_t)(quad * 32) << 16) + L::COL_S;
-        // out_scale l^|i-j| of row i against the columns of block jb: 32 consecutive
-        // entries of a table, neighbouring lanes one apart
-        const float* near = sNear + (rev ? 32 : kBlk - 1) - (32 * quad + lane);
-        const uint32_t diag = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
-        // this warp's part among the four of half a chunk, row of it, 16-byte column
-        const int part = warp >> 1, r = (lane & 7) + 8 * (warp & 1), ch = lane >> 3;
+    } else if (warp >= kOutputs) {
+        // ------------------------------------------------------ MMA issue ----
+        constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);
+        constexpr uint32_t id_pv = tc::idesc_bf16_f32(128, VP, 0, 1);
+        constexpr uint32_t id_qh = tc::idesc_bf16_f32(128, VP, 0, kLaneV ? 0 : 1);
+        constexpr uint32_t id_z = tc::idesc_bf16_f32(128, L::kXW, 1, 1);
+        const uint32_t base = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const int chunks = __shfl_sync(0xffffffffu, nch, 0);
+        const uint32_t kmaj = desc_lo(base, 16);       // rows contiguous along the contraction
+        const uint32_t mnmaj = desc_lo(base, kPanel);  // contraction along the rows
+        const uint32_t lead = tc::elect_one();
         bool ok = true;
+        if (warp == kScores) {
+#pragma unroll 1
+            for (int c = 0; kOut && c < chunks; ++c) {
+                const auto bq = L::buf(c, 0, kOut), bk = L::buf(c, 1, kOut);
+                // the scores overwrite the P that P V of the chunk kS before read
+                ok = wait_warp(&bars->full[bq.i], bq.use & 1) && wait_warp(&bars->full[bk.i], bk.use & 1) &&
+                     (c < L::kS || wait_warp(&bars->s_free[c % L::kS], (c / L::kS - 1) & 1));
+                if (!ok) break;
+                tc::tc_fence_after();
+                const uint32_t dq = kmaj + (bq.off >> 4), dk = kmaj + (bk.off >> 4);
+                const uint32_t d = tm + L::COL_S + (c % L::kS) * 128;
+#pragma unroll 4
+                for (int kk = 0; kk < KP / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
+                    tc::mma_ss_if(lead, d, desc(dq, off), desc(dk, off), id_s, kk > 0);
+                }
+                tc::mma_commit_if(lead, &bars->s_full[c & 1]);
+                release(lead, bq.i, 1);
+                release(lead, bk.i, 1);
+            }
+        } else if (warp == kOutputs) {
+#pragma unroll 1
+            for (int c = 0; kOut && c < chunks; ++c) {
+                const auto bq = L::buf(c, 0, kOut), bv = L::buf(c, 2, kOut);
+                // Q H
+                ok = wait_warp(&bars->full[bq.i], bq.use & 1) && wait_warp(&bars->h_full, c & 1) &&
+                     (c == 0 || wait_warp(&bars->o_free, (c - 1) & 1));
+                if (!ok) break;
+                tc::tc_fence_after();
+                const uint32_t dq = kmaj + (bq.off >> 4);
+#pragma unroll 4
+                for (int kk = 0; kk < KP / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
+                    const uint64_t dh = kLaneV ? desc(kmaj, L::OFF_H + off) : desc(mnmaj, L::OFF_H + kk * 2048);
+                    tc::mma_ss_if(lead, tm + L::COL_O2, desc(dq, off), dh, id_qh, kk > 0);
+                }
+                tc::mma_commit_if(lead, &bars->h_free);
+                release(lead, bq.i, 2);
+                // P V
+                ok = wait_warp(&bars->full[bv.i], bv.use & 1) &&
+                     wait_warp(&bars->p_full[c % L::kS], (c / L::kS) & 1) &&
+                     (chunk_n(chunk_at(c)) == kBlk || wait_warp(&bars->clean, 0));
+                if (!ok) break;
+                tc::tc_fence_after();
+                const uint32_t dv = mnmaj + (bv.off >> 4);
+                const uint32_t a = tm + L::COL_S + (c % L::kS) * 128;
+#pragma unroll 4
+                for (int kk = 0; kk < kBlk / 16; ++kk)
+                    tc::mma_ts_if(lead, tm + L::COL_O1, a + kk * 8, desc(dv, kk * 2048), id_pv, kk > 0);
+                tc::mma_commit_if(lead, &bars->o_full);
+                tc::mma_commit_if(lead, &bars->s_free[c % L::kS]);
+                release(lead, bv.i, 1);
+            }
+        } else {
+            const uint32_t partmn = desc_lo(base + L::OFF_PART, kPartPanel);
+#pragma unroll 1
+            for (int c = 0; ok && c < chunks; ++c) {
+                const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
+                ok = wait_warp(&bars->full[bk.i], bk.use & 1) && wait_warp(&bars->full[bv.i], bv.use & 1) &&
+                     (c < L::kZ || wait_warp(&bars->z_free[c % L::kZ], (c / L::kZ - 1) & 1)) &&
+                     (chunk_n(chunk_at(c)) == kBlk || wait_warp(&bars->clean, 0));
+                if (!ok) break;
+                tc::tc_fence_after();
+                // the operand that stays whole fills the MMA's rows
+                const uint32_t whole = mnmaj + ((L::kScaleV ? bk.off : bv.off) >> 4);
+                const uint32_t inplace = mnmaj + (bk.off >> 4);
+                const uint32_t z = tm + L::COL_Z + (c % L::kZ) * 64;
+#pragma unroll 1
+                for (int u = 0; u < kGroups; ++u) {
+                    const uint32_t g = (uint32_t)kGroups * c + u, s = g % L::kGroupBufs;
+                    ok = wait_warp(&bars->x_full[s], (g / L::kGroupBufs) & 1);
+                    if (!ok) break;
+                    const uint32_t da = whole + ((u * 2 * kPartPanel) >> 4);
+                    const uint32_t di = inplace + ((u * 2 * kPartPanel) >> 4);
+                    const uint32_t dx = partmn + ((s * 2 * L::kPartB) >> 4);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int x = 0; x < kPieces; ++x)
+                            tc::mma_ss_if(lead, z, desc(da, i * kPartPanel),
+                                          x < L::kFirst ? desc(di, i * kPartPanel)
+                                                        : desc(dx, i * L::kPartB + (x - L::kFirst) * L::kPieceB),
+                                          id_z, (u > 0 || i > 0 || x > 0) ? 1u : 0u);
+                    tc::mma_commit_if(lead, &bars->x_free[s]);
+                }
+                if (!ok) break;
+                tc::mma_commit_if(lead, &bars->z_full[c % L::kZ]);
+                release(lead, bk.i, 2);
+                release(lead, bv.i, 1);
+            }
+        }
+        if (!ok) fail();
+        // every product issued must be complete before TMEM is released
+        uint64_t* done = warp == kOutputs ? &bars->done : warp == kScores ? &bars->s_done : &bars->z_done;
+        tc::mma_commit_if(lead, done);
+        tc::mbar_wait(done, 0, nullptr, 200000000ull);
+    } else if (warp < 4) {
+        give();
+        if (kOut) {
+            // ------------------------------------- P = S o L, thread = row ----
+            const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16) + L::COL_S;
+            // out_scale l^|i-j| of row i against the columns of block jb: 32 consecutive
+            // entries of a table, neighbouring lanes one apart
+            const float* near = sNear + (rev ? 32 : kBlk - 1) - (32 * warp + lane);
+            const uint32_t diag = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+            bool ok = true;
+#pragma unroll 1
+            for (int c = 0; c < nch; ++c) {
+                const int n = chunk_n(chunk_at(c));
+                const uint32_t tc0 = ts + (c % L::kS) * 128;
+                ok = wait_warp(&bars->s_full[c & 1], (c >> 1) & 1);
+                if (!ok) break;
+                tc::tc_fence_after();
+#pragma unroll 1
+                for (int jb = 0; jb < 4; ++jb) {
+                    // the block's columns on the causal side and in the chunk
+                    uint32_t m = jb == warp ? diag : (rev ? jb > warp : jb < warp) ? 0xffffffffu : 0u;
+                    if (n < 32 * jb + 32) m &= n > 32 * jb ? 0xffffffffu >> (32 * jb + 32 - n) : 0u;
+                    uint32_t r[16];
+                    if (__any_sync(0xffffffffu, m != 0)) {
+                        float s[32];
+                        tc::tmem_ld32(tc0 + 32 * jb, s);
+                        const float* w = near + 32 * jb;
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 v = tc::mul2(make_float2(s[2 * j], s[2 * j + 1]), make_float2(w[2 * j], w[2 * j + 1]));
+                            s[2 * j] = v.x;
+                            s[2 * j + 1] = v.y;
+                        }
+                        // a product with 0 would keep a NaN of a masked place
+                        if (!__all_sync(0xffffffffu, m == 0xffffffffu)) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) s[j] = (m >> j) & 1 ? s[j] : 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) r[j] = tc::pack_bf16x2(s[2 * j], s[2 * j + 1]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) r[j] = 0;
+                    }
+                    // columns 16 jb .. overlay scores of blocks that are read
+                    tc::tmem_st16(tc0 + 16 * jb, r);
+                }
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars->p_full[c % L::kS]);
+            }
+            if (!ok) fail();
+        }
+    } else if (warp < 8) {
+        // ------------------------------------- w o K or w o V in pieces ----
+        give();
+        const int t = threadIdx.x - 128;
+        const int r = lane & 15, ch = lane >> 4;  // row of a part, first of its 16-byte columns
+        bool ok = true;
+        const int part = warp & 1, group0 = (warp - 4) >> 1;  // warps 4, 5: groups 0 and 2 of a chunk
 #pragma unroll 1
         for (int c = 0; ok && c < nch; ++c) {
             const int n = chunk_n(chunk_at(c));
@@ -474,10 +520,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             if (!ok) break;
             if (n < kBlk) {
                 const int each = (kBlk - n) * 8;
-                for (int e = threadIdx.x; e < each * (KP / 64 + VP / 64); e += 256) {
+                for (int e = t; e < each * (KP / 64 + VP / 64); e += 128) {
                     const int x = e / each, f = e - x * each;
                     const uint32_t off = x < KP / 64 ? bk.off + x * kPanel : bv.off + (x - KP / 64) * kPanel;
-                    // where pieces go in place, the rows belong to their part's warps
+                    // rows of a part belong to its warp where pieces go in place
                     if (!(L::kRing && x < KP / 64))
                         *reinterpret_cast<uint4*>(sm + off + (n + f / 8) * 128 + (f & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
@@ -486,28 +532,29 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 if (lane == 0) tc::mbar_arrive(&bars->clean);
             }
 #pragma unroll 1
-            for (int hc = 0; hc < 2; ++hc) {
-                const int u = 2 * hc + (part >> 1);  // group of the chunk
+            for (int u = group0; u < kGroups; u += 2) {
                 const uint32_t g = (uint32_t)kGroups * c + u, s = g % L::kGroupBufs;
                 if (g >= L::kGroupBufs) {
                     ok = wait_warp(&bars->x_free[s], (g / L::kGroupBufs - 1) & 1);
                     if (!ok) break;
                 }
-                const int row = 64 * hc + kPartT * part + r;
+                const int row = kPartT * (2 * u + part) + r;
                 const bool inside = row < n;
                 const float w = inside ? sTab[rev ? row : n - 1 - row] : 0.f;
                 const float2 w2 = make_float2(w, w), minus = make_float2(-1.f, -1.f);
                 uint8_t* src = sm + bx.off + row * 128;
-                uint8_t* out = sm + L::OFF_PART + (2 * s + (part & 1)) * L::kPartB + r * 128;
-#pragma unroll
+                uint8_t* out = sm + L::OFF_PART + (2 * s + part) * L::kPartB + r * 128;
+#pragma unroll 1
                 for (int x = 0; x < L::kXW / 64; ++x) {
+                    uint4 v[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        // eight neighbouring rows take eight different 16-byte columns
-                        const int cc = ((4 * i + ch) ^ (r & 7)) * 16;
-                        uint4 v = *reinterpret_cast<const uint4*>(src + x * kPanel + cc);
-                        if (!inside) v = make_uint4(0, 0, 0, 0);
-                        const uint32_t in4[4] = {v.x, v.y, v.z, v.w};
+                    for (int i = 0; i < 4; ++i)  // eight neighbouring rows take eight different 16-byte columns
+                        v[i] = *reinterpret_cast<const uint4*>(src + x * kPanel + ((2 * i + ch) ^ (r & 7)) * 16);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int cc = ((2 * i + ch) ^ (r & 7)) * 16;
+                        if (!inside) v[i] = make_uint4(0, 0, 0, 0);
+                        const uint32_t in4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                         uint32_t q[kPieces][4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -516,8 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                             for (int y = 0; y + 1 < kPieces; ++y) {
                                 // the leading 8 bits of each, and what they leave (exactly)
                                 q[y][e] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-                                f = tc::fma2(make_float2(__uint_as_float(__float_as_uint(f.x) & 0xffff0000u),
-                                                         __uint_as_float(__float_as_uint(f.y) & 0xffff0000u)), minus, f);
+                                f = tc::fma2(tc::unpack_bf16x2(q[y][e]), minus, f);
                             }
                             q[kPieces - 1][e] = tc::pack_bf16x2(f.x, f.y);
                         }
@@ -531,50 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars->x_full[s]);
-                if (!kOut || hc == 1) continue;
-                const uint32_t tc0 = ts + (c % L::kS) * 128;
-                ok = wait_warp(&bars->s_full[c & 1], (c >> 1) & 1);
-                if (!ok) break;
-                tc::tc_fence_after();
-#pragma unroll 1
-                for (int jb = 2 * half; jb < 2 * half + 2; ++jb) {
-                    // the block's columns on the causal side and in the chunk
-                    uint32_t m = jb == quad ? diag : (rev ? jb > quad : jb < quad) ? 0xffffffffu : 0u;
-                    if (n < 32 * jb + 32) m &= n > 32 * jb ? 0xffffffffu >> (32 * jb + 32 - n) : 0u;
-                    uint32_t pr[16];
-                    if (__any_sync(0xffffffffu, m != 0)) {
-                        float sc[32];
-                        tc::tmem_ld32(tc0 + 32 * jb, sc);
-                        const float* wl = near + 32 * jb;
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float2 y = tc::mul2(make_float2(sc[2 * j], sc[2 * j + 1]), make_float2(wl[2 * j], wl[2 * j + 1]));
-                            sc[2 * j] = y.x;
-                            sc[2 * j + 1] = y.y;
-                        }
-                        // a product with 0 would keep a NaN of a masked place
-                        if (!__all_sync(0xffffffffu, m == 0xffffffffu)) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) sc[j] = (m >> j) & 1 ? sc[j] : 0.f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) pr[j] = tc::pack_bf16x2(sc[2 * j], sc[2 * j + 1]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) pr[j] = 0;
-                    }
-                    // each half's P overlays scores of its own that are read
-                    tc::tmem_st16(tc0 + 64 * half + 16 * (jb & 1), pr);
-                }
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->p_full[c % L::kS]);
             }
         }
         if (!ok) fail();
-    } else if (warp < 16) {
+    } else if (warp < kState + kStateWarps) {
         // ------------------------------------------------ state and output ----
         take();
         const int quad = warp & 3, half = (warp - 8) >> 2;
@@ -736,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 17) {
+    if (warp == kOutputs) {
         __syncwarp();
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
