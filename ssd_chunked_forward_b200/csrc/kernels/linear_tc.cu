@@ -22,10 +22,10 @@
 // its rounding would grow with the number of chunks.
 //
 // Warp roles (640 threads):
-//   0-3    scores -> P (thread = row i)
-//   4-7    w o K or w o V in pieces: parts of 16 tokens, each a warp's own, two parts
-//          to a buffer and a hand-over; rows behind a partial chunk's end become
-//          zeros in K and V (with packed sequences they hold the next one's tokens)
+//   0-3    scores -> P (thread = row i), and the last quarter of
+//   4-7    w o K or w o V in pieces: groups of 32 tokens, four warps to each; rows
+//          behind a partial chunk's end become zeros in K and V (with packed
+//          sequences they hold the next one's tokens)
 //   8-15   state and output, two warps to a TMEM lane quadrant
 //   16     lane 0 loads tiles by TMA; lane 1 stores output tiles (plain stores of rows
 //          by their threads touch 32 lines each and kept the load/store unit busy
@@ -57,13 +57,15 @@ constexpr int kPartT = 16;               // tokens of a part: the MMA's K
 constexpr uint32_t kPartPanel = kPartT * 128;
 constexpr int kGroups = kBlk / (2 * kPartT);  // a chunk's groups of two parts
 
-constexpr int kMaxBufs = 9, kMaxGroupBufs = 4;
+constexpr int kMaxBufs = 9;
 struct __align__(8) Bars {
     uint64_t full[kMaxBufs], empty[kMaxBufs];
     // s_full alternates even with one score buffer: the next chunk's S may be done
     // before the warps that make the pieces have seen this one's
     uint64_t s_full[2], s_free[2], p_full[2], o_full, o_free;
-    uint64_t x_full[kMaxGroupBufs], x_free[kMaxGroupBufs], clean;
+    // by group of the chunk, not by buffer: a warp then waits for every phase of a
+    // barrier that it waits on
+    uint64_t x_full[kGroups], x_free[kGroups], clean;
     uint64_t z_full[2], z_free[2], h_full, h_free, staged, stored;
     uint64_t done, z_done, s_done;
 };
@@ -217,11 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         }
         tc::mbar_init(&bars->o_full, 1);
         tc::mbar_init(&bars->o_free, kStateWarps);
-        for (int i = 0; i < kMaxGroupBufs; ++i) {
-            tc::mbar_init(&bars->x_full[i], 2);
+        for (int i = 0; i < kGroups; ++i) {
+            tc::mbar_init(&bars->x_full[i], 4);
             tc::mbar_init(&bars->x_free[i], 1);
         }
-        tc::mbar_init(&bars->clean, 4);
+        tc::mbar_init(&bars->clean, 8);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars->z_full[i], 1);
             tc::mbar_init(&bars->z_free[i], kStateWarps);
@@ -286,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     if (warp == kLoads) {
         if (lane == 0) {
             // ------------------------------------------------- TMA loads ----
+            // (unrolled: with rolled loops the loads went out later, 40 us of 450)
             bool ok = true;
             const int hq = it.head / R.q.share;
             const int hk = it.head / R.k.share, hv = it.head / R.v.share;
@@ -293,13 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
 #pragma unroll 1
             for (; ok && c < nch; ++c) {
                 const int row = (int)(it.row0 + chunk_at(c));
-#pragma unroll 1
+#pragma unroll
                 for (int w = kOut ? 0 : 1; w < 3; ++w) {
                     const auto b = L::buf(c, w, kOut);
                     if (b.use > 0 && !wait(&bars->empty[b.i], (b.use - 1) & 1)) { ok = false; break; }
                     const int panels = (w == 2 ? VP : KP) / 64;
                     tc::mbar_arrive_expect_tx(&bars->full[b.i], panels * kPanel);
-#pragma unroll 1
                     for (int x = 0; x < panels; ++x)
                         tc::tma_load_4d(sm + b.off + x * kPanel, &p.map[it.role][w], &bars->full[b.i], 64 * x,
                                         w == 0 ? hq : w == 1 ? hk : hv, row, it.batch);
@@ -418,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 const uint32_t z = tm + L::COL_Z + (c % L::kZ) * 64;
 #pragma unroll 1
                 for (int u = 0; u < kGroups; ++u) {
-                    const uint32_t g = (uint32_t)kGroups * c + u, s = g % L::kGroupBufs;
-                    ok = wait_warp(&bars->x_full[s], (g / L::kGroupBufs) & 1);
+                    const uint32_t s = u % L::kGroupBufs;
+                    ok = wait_warp(&bars->x_full[u], c & 1);
                     if (!ok) break;
                     const uint32_t da = whole + ((u * 2 * kPartPanel) >> 4);
                     const uint32_t di = inplace + ((u * 2 * kPartPanel) >> 4);
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                                           x < L::kFirst ? desc(di, i * kPartPanel)
                                                         : desc(dx, i * L::kPartB + (x - L::kFirst) * L::kPieceB),
                                           id_z, (u > 0 || i > 0 || x > 0) ? 1u : 0u);
-                    tc::mma_commit_if(lead, &bars->x_free[s]);
+                    tc::mma_commit_if(lead, &bars->x_free[u]);
                 }
                 if (!ok) break;
                 tc::mma_commit_if(lead, &bars->z_full[c % L::kZ]);
@@ -445,19 +447,42 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         uint64_t* done = warp == kOutputs ? &bars->done : warp == kScores ? &bars->s_done : &bars->z_done;
         tc::mma_commit_if(lead, done);
         tc::mbar_wait(done, 0, nullptr, 200000000ull);
-    } else if (warp < 4) {
+    } else if (warp < 8) {
+        // ------------------------------------------------- P, thread = row ----
+        // --------------------------------- and w o K or w o V in pieces ----
         give();
-        if (kOut) {
-            // ------------------------------------- P = S o L, thread = row ----
-            const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16) + L::COL_S;
-            // out_scale l^|i-j| of row i against the columns of block jb: 32 consecutive
-            // entries of a table, neighbouring lanes one apart
-            const float* near = sNear + (rev ? 32 : kBlk - 1) - (32 * warp + lane);
-            const uint32_t diag = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
-            bool ok = true;
+        const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16) + L::COL_S;
+        // out_scale l^|i-j| of row i against the columns of block jb: 32 consecutive
+        // entries of a table, neighbouring lanes one apart
+        const float* near = sNear + (rev ? 32 : kBlk - 1) - (32 * warp + lane);
+        const uint32_t diag = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+        // four warps to a group: its part, the row of it, the first 16-byte column
+        const int part = (warp >> 1) & 1, r = (lane & 7) + 8 * (warp & 1), ch = lane >> 3;
+        bool ok = true;
 #pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
-                const int n = chunk_n(chunk_at(c));
+        for (int c = 0; ok && c < nch; ++c) {
+            const int n = chunk_n(chunk_at(c));
+            const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
+            const auto bx = L::kScaleV ? bv : bk;
+            if (n < kBlk) {
+                // k's rows behind the end: the scores' columns there are masked,
+                // whatever they are
+                ok = wait_warp(&bars->full[bk.i], bk.use & 1) && wait_warp(&bars->full[bv.i], bv.use & 1) &&
+                     (!kOut || wait_warp(&bars->s_full[c & 1], (c >> 1) & 1));
+                if (!ok) break;
+                const int each = (kBlk - n) * 8;
+                for (int e = threadIdx.x; e < each * (KP / 64 + VP / 64); e += 256) {
+                    const int x = e / each, f = e - x * each;
+                    const uint32_t off = x < KP / 64 ? bk.off + x * kPanel : bv.off + (x - KP / 64) * kPanel;
+                    // where pieces go in place, the rows belong to their part's warps
+                    if (!(L::kRing && x < KP / 64))
+                        *reinterpret_cast<uint4*>(sm + off + (n + f / 8) * 128 + (f & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars->clean);
+            }
+            if (kOut && warp < 4) {
                 const uint32_t tc0 = ts + (c % L::kS) * 128;
                 ok = wait_warp(&bars->s_full[c & 1], (c >> 1) & 1);
                 if (!ok) break;
@@ -498,44 +523,20 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars->p_full[c % L::kS]);
             }
-            if (!ok) fail();
-        }
-    } else if (warp < 8) {
-        // ------------------------------------- w o K or w o V in pieces ----
-        give();
-        const int t = threadIdx.x - 128;
-        const int r = lane & 15, ch = lane >> 4;  // row of a part, first of its 16-byte columns
-        bool ok = true;
-        const int part = warp & 1, group0 = (warp - 4) >> 1;  // warps 4, 5: groups 0 and 2 of a chunk
-#pragma unroll 1
-        for (int c = 0; ok && c < nch; ++c) {
-            const int n = chunk_n(chunk_at(c));
-            const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
-            const auto bx = L::kScaleV ? bv : bk;
-            ok = wait_warp(&bars->full[bx.i], bx.use & 1);
-            // k's place is overwritten: by the first piece in the ring, and behind a
-            // partial chunk's end (the scores' columns there are masked, whatever they are)
-            if (kOut && (L::kRing || n < kBlk)) ok = ok && wait_warp(&bars->s_full[c & 1], (c >> 1) & 1);
-            if (n < kBlk) ok = ok && wait_warp(&bars->full[bk.i], bk.use & 1) && wait_warp(&bars->full[bv.i], bv.use & 1);
+            ok = wait_warp(&bars->full[bx.i], bx.use & 1) &&
+                 // in the ring the first piece takes k's place: the scores have read it
+                 (!(kOut && L::kRing) || wait_warp(&bars->s_full[c & 1], (c >> 1) & 1));
             if (!ok) break;
-            if (n < kBlk) {
-                const int each = (kBlk - n) * 8;
-                for (int e = t; e < each * (KP / 64 + VP / 64); e += 128) {
-                    const int x = e / each, f = e - x * each;
-                    const uint32_t off = x < KP / 64 ? bk.off + x * kPanel : bv.off + (x - KP / 64) * kPanel;
-                    // rows of a part belong to its warp where pieces go in place
-                    if (!(L::kRing && x < KP / 64))
-                        *reinterpret_cast<uint4*>(sm + off + (n + f / 8) * 128 + (f & 7) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->clean);
-            }
+            // warps 0-3 make P and the last group, 4-7 the other three; without P
+            // every other group each
+            const int u0 = kOut ? (warp < 4 ? 3 : 0) : (warp < 4 ? 1 : 0), u1 = kOut && warp >= 4 ? 3 : kGroups;
 #pragma unroll 1
-            for (int u = group0; u < kGroups; u += 2) {
-                const uint32_t g = (uint32_t)kGroups * c + u, s = g % L::kGroupBufs;
-                if (g >= L::kGroupBufs) {
-                    ok = wait_warp(&bars->x_free[s], (g / L::kGroupBufs - 1) & 1);
+            for (int u = u0; u < u1; u += kOut ? 1 : 2) {
+                const uint32_t s = u % L::kGroupBufs;
+                // the buffer's last group: of this chunk, or of the one before
+                const int before = (u + kGroups - L::kGroupBufs) % kGroups, cb = before < u ? c : c - 1;
+                if (cb >= 0) {
+                    ok = wait_warp(&bars->x_free[before], cb & 1);
                     if (!ok) break;
                 }
                 const int row = kPartT * (2 * u + part) + r;
@@ -544,39 +545,35 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 const float2 w2 = make_float2(w, w), minus = make_float2(-1.f, -1.f);
                 uint8_t* src = sm + bx.off + row * 128;
                 uint8_t* out = sm + L::OFF_PART + (2 * s + part) * L::kPartB + r * 128;
-#pragma unroll 1
-                for (int x = 0; x < L::kXW / 64; ++x) {
-                    uint4 v[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)  // eight neighbouring rows take eight different 16-byte columns
-                        v[i] = *reinterpret_cast<const uint4*>(src + x * kPanel + ((2 * i + ch) ^ (r & 7)) * 16);
+                for (int i = 0; i < L::kXW / 32; ++i) {
+                    // eight neighbouring rows take eight different 16-byte columns
+                    const int x = i >> 1, cc = ((4 * (i & 1) + ch) ^ (r & 7)) * 16;
+                    uint4 v = *reinterpret_cast<const uint4*>(src + x * kPanel + cc);
+                    if (!inside) v = make_uint4(0, 0, 0, 0);
+                    const uint32_t in4[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t q[kPieces][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int cc = ((2 * i + ch) ^ (r & 7)) * 16;
-                        if (!inside) v[i] = make_uint4(0, 0, 0, 0);
-                        const uint32_t in4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        uint32_t q[kPieces][4];
+                    for (int e = 0; e < 4; ++e) {
+                        float2 f = tc::mul2(tc::unpack_bf16x2(in4[e]), w2);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float2 f = tc::mul2(tc::unpack_bf16x2(in4[e]), w2);
-#pragma unroll
-                            for (int y = 0; y + 1 < kPieces; ++y) {
-                                // the leading 8 bits of each, and what they leave (exactly)
-                                q[y][e] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-                                f = tc::fma2(tc::unpack_bf16x2(q[y][e]), minus, f);
-                            }
-                            q[kPieces - 1][e] = tc::pack_bf16x2(f.x, f.y);
+                        for (int y = 0; y + 1 < kPieces; ++y) {
+                            // the leading 8 bits of each, and what they leave (exactly)
+                            q[y][e] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+                            f = tc::fma2(make_float2(__uint_as_float(__float_as_uint(f.x) & 0xffff0000u),
+                                                     __uint_as_float(__float_as_uint(f.y) & 0xffff0000u)), minus, f);
                         }
+                        q[kPieces - 1][e] = tc::pack_bf16x2(f.x, f.y);
+                    }
 #pragma unroll
-                        for (int y = 0; y < kPieces; ++y) {
-                            uint8_t* to = y < L::kFirst ? src + x * kPanel : out + (y - L::kFirst) * L::kPieceB + x * kPartPanel;
-                            *reinterpret_cast<uint4*>(to + cc) = make_uint4(q[y][0], q[y][1], q[y][2], q[y][3]);
-                        }
+                    for (int y = 0; y < kPieces; ++y) {
+                        uint8_t* to = y < L::kFirst ? src + x * kPanel : out + (y - L::kFirst) * L::kPieceB + x * kPartPanel;
+                        *reinterpret_cast<uint4*>(to + cc) = make_uint4(q[y][0], q[y][1], q[y][2], q[y][3]);
                     }
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->x_full[s]);
+                if (lane == 0) tc::mbar_arrive(&bars->x_full[u]);
             }
         }
         if (!ok) fail();
