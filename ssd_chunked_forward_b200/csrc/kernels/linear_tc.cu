@@ -116,9 +116,15 @@ struct Layout {
     static_assert(kBytes <= 232448, "shared memory above the 227 KB per-block limit");
     static_assert(OFF_PART % 1024 == 0 && OFF_H % 1024 == 0 && OFF_OUT % 1024 == 0, "swizzled tiles start on 1024 bytes");
 
-    // TMEM columns: scores (P in their first 64), P V, Q H, Z
+    // TMEM columns: scores (P in their first 64), P V, Q H, Z.  (Tried with V = 64:
+    // P beside one score buffer and all pieces' products side by side, which reads
+    // 64 KB less of shared memory a chunk: 5 % slower at K = 128, 20 % at K = 64,
+    // since the scores no longer run a chunk ahead.)
     static constexpr int kS = VP == 64 ? 2 : 1;
     static constexpr int kZ = VP == 64 ? 2 : 1;
+    // K = 64, V = 128 has columns for two pieces side by side: one MMA reads the whole
+    // operand for both, the third piece is added to the second's columns
+    static constexpr int kSide = KP == 64 && VP == 128 ? 2 : 1;
     static constexpr uint32_t COL_S = 0, COL_O1 = 128 * kS, COL_O2 = COL_O1 + VP, COL_Z = 384;
 
     // buffer, its use count and its place, of tile `which` (0 q, 1 k, 2 v) of chunk c;
@@ -343,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);
         constexpr uint32_t id_pv = tc::idesc_bf16_f32(128, VP, 0, 1);
         constexpr uint32_t id_qh = tc::idesc_bf16_f32(128, VP, 0, kLaneV ? 0 : 1);
-        constexpr uint32_t id_z = tc::idesc_bf16_f32(128, L::kXW, 1, 1);
+        constexpr uint32_t id_z = tc::idesc_bf16_f32(128, L::kSide * L::kXW, 1, 1);
+        constexpr uint32_t id_z1 = tc::idesc_bf16_f32(128, L::kXW, 1, 1);
         const uint32_t base = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const int chunks = __shfl_sync(0xffffffffu, nch, 0);
@@ -429,11 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int x = 0; x < kPieces; ++x)
-                            tc::mma_ss_if(lead, z, desc(da, i * kPartPanel),
+                        for (int x = 0; x < kPieces; x += x == 0 ? L::kSide : 1)
+                            tc::mma_ss_if(lead, x == 0 ? z : z + (L::kSide - 1) * L::kXW, desc(da, i * kPartPanel),
                                           x < L::kFirst ? desc(di, i * kPartPanel)
                                                         : desc(dx, i * L::kPartB + (x - L::kFirst) * L::kPieceB),
-                                          id_z, (u > 0 || i > 0 || x > 0) ? 1u : 0u);
+                                          x == 0 ? id_z : id_z1, (u > 0 || i > 0 || x > 0) ? 1u : 0u);
                     tc::mma_commit_if(lead, &bars->x_free[u]);
                 }
                 if (!ok) break;
@@ -527,9 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                  // in the ring the first piece takes k's place: the scores have read it
                  (!(kOut && L::kRing) || wait_warp(&bars->s_full[c & 1], (c >> 1) & 1));
             if (!ok) break;
-            // warps 0-3 make P and the last group, 4-7 the other three; without P
-            // every other group each
-            const int u0 = kOut ? (warp < 4 ? 3 : 0) : (warp < 4 ? 1 : 0), u1 = kOut && warp >= 4 ? 3 : kGroups;
+            // warps 0-3 make P and, with V = 128, the last group, 4-7 the others;
+            // without P every other group each
+            constexpr int kMine = VP == 64 ? kGroups : kGroups - 1;
+            const int u0 = kOut ? (warp < 4 ? kMine : 0) : (warp < 4 ? 1 : 0), u1 = kOut && warp >= 4 ? kMine : kGroups;
 #pragma unroll 1
             for (int u = u0; u < u1; u += kOut ? 1 : 2) {
                 const uint32_t s = u % L::kGroupBufs;
@@ -631,16 +639,23 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             const float2 dec = sDec[c == 0 ? 1 : c + 1 == nch ? 2 : 0];
             const float2 dx = make_float2(dec.x, dec.x), dy = make_float2(dec.y, dec.y);
 #pragma unroll
-            for (int x = 0; x < CH / 32; ++x) {
-                float z[32];
-                tc::tmem_ld32(tl + L::COL_Z + (c % L::kZ) * 64 + c0 + 32 * x, z);
+            for (int x = 0; x < CH / 16; ++x) {
+                float z[L::kSide][16];
+#pragma unroll
+                for (int y = 0; y < L::kSide; ++y)
+                    tc::tmem_ld16(tl + L::COL_Z + (c % L::kZ + y) * 64 + c0 + 16 * x, z[y]);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float2 o = make_float2(h[32 * x + e], h[32 * x + e + 1]);
-                    const float2 w = tc::fma2(o, dx, tc::fma2(o, dy, make_float2(z[e], z[e + 1])));
-                    h[32 * x + e] = w.x;
-                    h[32 * x + e + 1] = w.y;
+                for (int e = 0; e < 16; e += 2) {
+                    float2 add = make_float2(z[0][e], z[0][e + 1]);
+                    if constexpr (L::kSide == 2) {
+                        add.x += z[1][e];
+                        add.y += z[1][e + 1];
+                    }
+                    const float2 o = make_float2(h[16 * x + e], h[16 * x + e + 1]);
+                    const float2 w = tc::fma2(o, dx, tc::fma2(o, dy, add));
+                    h[16 * x + e] = w.x;
+                    h[16 * x + e + 1] = w.y;
                 }
             }
             tc::tc_fence_before();
