@@ -57,7 +57,7 @@ constexpr int kPartT = 16;               // tokens of a part: the MMA's K
 constexpr uint32_t kPartPanel = kPartT * 128;
 constexpr int kGroups = kBlk / (2 * kPartT);  // a chunk's groups of two parts
 
-constexpr int kMaxBufs = 9;
+constexpr int kMaxBufs = 10;
 struct __align__(8) Bars {
     uint64_t full[kMaxBufs], empty[kMaxBufs];
     // s_full alternates even with one score buffer: the next chunk's S may be done
@@ -85,28 +85,32 @@ struct TcParams {
     ScanLaunch s;
 };
 
-// Shared and tensor memory of a variant.  K = V = 128: a ring of five tiles in
-// the order q, k, v, q, ... (a whole second chunk does not fit); the first piece
-// of w o K goes into K's own place once the scores are done, and the output
-// tile into V's.  The others hold whole chunks, all pieces and an output tile.
-template <int KP, int VP, int kPieces>
+// Shared and tensor memory of a variant.  K = V = 128: the first piece of w o K
+// goes into K's own place once the scores are done; with outputs, a ring of
+// kSlots tiles in the order q, k, v, q, ... (a whole second chunk does not fit), the
+// output tile in V's place.  The others hold whole chunks, all pieces and an
+// output tile; a scan for states alone holds k and v of whole chunks.
+template <int KP, int VP, bool kOut, int kPieces>
 struct Layout {
-    static constexpr bool kRing = KP == 128 && VP == 128;
+    static constexpr bool kInPlace = KP == 128 && VP == 128, kRing = kInPlace && kOut;
+    static constexpr int kSlots = 5;
     static constexpr uint32_t kKB = KP / 64 * kPanel, kVB = VP / 64 * kPanel;
-    static constexpr uint32_t kChunk = 2 * kKB + kVB;
-    static constexpr int kStages = kRing ? 0 : KP == 64 && VP == 64 ? 3 : 2;
-    static constexpr int kBufs = kRing ? 5 : 3 * kStages;
-    // the scaled operand and its parts: pieces first .. kPieces - 1 in buffers
+    static constexpr uint32_t kChunk = (kOut ? 2 : 1) * kKB + kVB;
+    static constexpr int kStages = kRing ? 0 : kOut ? (KP == 64 && VP == 64 ? 3 : 2) : kInPlace ? 2 : KP + VP == 128 ? 5 : 3;
+    static constexpr int kTiles = kOut ? 3 : 2;  // of a chunk
+    static constexpr int kBufs = kRing ? kSlots : kTiles * kStages;
+    static_assert(kBufs <= kMaxBufs, "barriers");
+    // the scaled operand and its parts: pieces kFirst .. kPieces - 1 in buffers
     static constexpr bool kScaleV = VP == 64;
-    static constexpr int kXW = kRing ? 128 : 64;
-    static constexpr int kFirst = kRing ? 1 : 0;
+    static constexpr int kXW = kInPlace ? 128 : 64;
+    static constexpr int kFirst = kInPlace ? 1 : 0;
     static constexpr uint32_t kPieceB = kXW / 64 * kPartPanel;
     static constexpr uint32_t kPartB = (kPieces - kFirst) * kPieceB;
-    static constexpr int kGroupBufs = kRing || KP == 128 ? 2 : 4;
-    static constexpr uint32_t OFF_PART = kRing ? 5 * 2 * kPanel : kStages * kChunk;
+    static constexpr int kGroupBufs = !kOut ? 4 : kRing ? 2 : KP == 128 ? 2 : 4;
+    static constexpr uint32_t OFF_PART = kRing ? kSlots * 2 * kPanel : kStages * kChunk;
     static constexpr uint32_t OFF_H = OFF_PART + 2 * kGroupBufs * kPartB;
-    static constexpr uint32_t OFF_OUT = OFF_H + (uint32_t)KP * VP * 2;
-    static constexpr uint32_t OFF_TAB = OFF_OUT + (kRing ? 0 : kVB);
+    static constexpr uint32_t OFF_OUT = OFF_H + (kOut ? (uint32_t)KP * VP * 2 : 0);
+    static constexpr uint32_t OFF_TAB = OFF_OUT + (kRing || !kOut ? 0 : kVB);
     static constexpr uint32_t OFF_NEAR = OFF_TAB + 132 * 4;
     static constexpr uint32_t OFF_DEC = OFF_NEAR + 160 * 4;
     static constexpr uint32_t OFF_BAR = OFF_DEC + 4 * 8;
@@ -130,18 +134,18 @@ struct Layout {
     // buffer, its use count and its place, of tile `which` (0 q, 1 k, 2 v) of chunk c;
     // a state-only scan loads no q
     struct Buf { uint32_t i, use, off; };
-    static __device__ __forceinline__ Buf buf(uint32_t c, uint32_t which, bool out) {
+    static __device__ __forceinline__ Buf buf(uint32_t c, uint32_t which) {
         Buf b;
-        if (kRing) {
-            const uint32_t n = out ? 3 * c + which : 2 * c + which - 1;
-            b.use = n / 5;
-            b.i = n - 5 * b.use;
+        if constexpr (kRing) {
+            const uint32_t n = 3 * c + which;
+            b.use = n / kSlots;
+            b.i = n - kSlots * b.use;
             b.off = b.i * 2 * kPanel;
         } else {
-            b.use = c / (uint32_t)(kStages ? kStages : 1);
-            const uint32_t st = c - b.use * kStages;
-            b.i = 3 * st + which;
-            b.off = st * kChunk + (which > 0 ? kKB : 0) + (which > 1 ? kKB : 0);
+            b.use = c / (uint32_t)kStages;
+            const uint32_t st = c - b.use * kStages, k = which - (3 - kTiles);  // k-th tile of its chunk
+            b.i = kTiles * st + k;
+            b.off = st * kChunk + (k > 0 ? kKB : 0) + (k > 1 ? kKB : 0);
         }
         return b;
     }
@@ -173,7 +177,7 @@ __device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity) {
 
 template <int KP, int VP, bool kOut, int kPieces>
 __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ TcParams p) {
-    using L = Layout<KP, VP, kPieces>;
+    using L = Layout<KP, VP, kOut, kPieces>;
     constexpr bool kLaneV = VP == 128;         // lanes of Z: v, else k
     constexpr int CH = kLaneV ? KP / 2 : 32;   // state columns of a thread
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 const int row = (int)(it.row0 + chunk_at(c));
 #pragma unroll
                 for (int w = kOut ? 0 : 1; w < 3; ++w) {
-                    const auto b = L::buf(c, w, kOut);
+                    const auto b = L::buf(c, w);
                     if (b.use > 0 && !wait(&bars->empty[b.i], (b.use - 1) & 1)) { ok = false; break; }
                     const int panels = (w == 2 ? VP : KP) / 64;
                     tc::mbar_arrive_expect_tx(&bars->full[b.i], panels * kPanel);
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 // no copy may still be landing in shared memory when the block exits
                 for (int cc = c > 4 ? c - 4 : 0; cc < c; ++cc)
                     for (int w = kOut ? 0 : 1; w < 3; ++w) {
-                        const auto b = L::buf(cc, w, kOut);
+                        const auto b = L::buf(cc, w);
                         tc::mbar_wait(&bars->full[b.i], b.use & 1, nullptr, 200000000ull);
                     }
             }
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             bool ok = true;
             for (int c = 0; c < nch; ++c) {
                 const int t = chunk_at(c);
-                const auto bv = L::buf(c, 2, kOut);
+                const auto bv = L::buf(c, 2);
                 ok = wait(&bars->staged, c & 1);
                 if (!ok) break;
                 if (!direct(chunk_n(t))) {
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         if (warp == kScores) {
 #pragma unroll 1
             for (int c = 0; kOut && c < chunks; ++c) {
-                const auto bq = L::buf(c, 0, kOut), bk = L::buf(c, 1, kOut);
+                const auto bq = L::buf(c, 0), bk = L::buf(c, 1);
                 // the scores overwrite the P that P V of the chunk kS before read
                 ok = wait_warp(&bars->full[bq.i], bq.use & 1) && wait_warp(&bars->full[bk.i], bk.use & 1) &&
                      (c < L::kS || wait_warp(&bars->s_free[c % L::kS], (c / L::kS - 1) & 1));
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         } else if (warp == kOutputs) {
 #pragma unroll 1
             for (int c = 0; kOut && c < chunks; ++c) {
-                const auto bq = L::buf(c, 0, kOut), bv = L::buf(c, 2, kOut);
+                const auto bq = L::buf(c, 0), bv = L::buf(c, 2);
                 // Q H
                 ok = wait_warp(&bars->full[bq.i], bq.use & 1) && wait_warp(&bars->h_full, c & 1) &&
                      (c == 0 || wait_warp(&bars->o_free, (c - 1) & 1));
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             const uint32_t partmn = desc_lo(base + L::OFF_PART, kPartPanel);
 #pragma unroll 1
             for (int c = 0; ok && c < chunks; ++c) {
-                const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
+                const auto bk = L::buf(c, 1), bv = L::buf(c, 2);
                 ok = wait_warp(&bars->full[bk.i], bk.use & 1) && wait_warp(&bars->full[bv.i], bv.use & 1) &&
                      (c < L::kZ || wait_warp(&bars->z_free[c % L::kZ], (c / L::kZ - 1) & 1)) &&
                      (chunk_n(chunk_at(c)) == kBlk || wait_warp(&bars->clean, 0));
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
 #pragma unroll 1
         for (int c = 0; ok && c < nch; ++c) {
             const int n = chunk_n(chunk_at(c));
-            const auto bk = L::buf(c, 1, kOut), bv = L::buf(c, 2, kOut);
+            const auto bk = L::buf(c, 1), bv = L::buf(c, 2);
             const auto bx = L::kScaleV ? bv : bk;
             if (n < kBlk) {
                 // k's rows behind the end: the scores' columns there are masked,
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     const int x = e / each, f = e - x * each;
                     const uint32_t off = x < KP / 64 ? bk.off + x * kPanel : bv.off + (x - KP / 64) * kPanel;
                     // where pieces go in place, the rows belong to their part's warps
-                    if (!(L::kRing && x < KP / 64))
+                    if (!(L::kInPlace && x < KP / 64))
                         *reinterpret_cast<uint4*>(sm + off + (n + f / 8) * 128 + (f & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
                 tc::fence_proxy_async_smem();
@@ -553,13 +557,15 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 const float2 w2 = make_float2(w, w), minus = make_float2(-1.f, -1.f);
                 uint8_t* src = sm + bx.off + row * 128;
                 uint8_t* out = sm + L::OFF_PART + (2 * s + part) * L::kPartB + r * 128;
+                uint4 v[L::kXW / 32];  // all loads before the first store (which may be to the same place)
+#pragma unroll
+                for (int i = 0; i < L::kXW / 32; ++i)  // eight neighbouring rows take eight different 16-byte columns
+                    v[i] = *reinterpret_cast<const uint4*>(src + (i >> 1) * kPanel + ((4 * (i & 1) + ch) ^ (r & 7)) * 16);
 #pragma unroll
                 for (int i = 0; i < L::kXW / 32; ++i) {
-                    // eight neighbouring rows take eight different 16-byte columns
                     const int x = i >> 1, cc = ((4 * (i & 1) + ch) ^ (r & 7)) * 16;
-                    uint4 v = *reinterpret_cast<const uint4*>(src + x * kPanel + cc);
-                    if (!inside) v = make_uint4(0, 0, 0, 0);
-                    const uint32_t in4[4] = {v.x, v.y, v.z, v.w};
+                    if (!inside) v[i] = make_uint4(0, 0, 0, 0);
+                    const uint32_t in4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                     uint32_t q[kPieces][4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -677,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 // the ring's tile takes the place of this chunk's V, consumed with z_full and
                 // o_full; the others' is free once the last one has left (waited for in both:
                 // no barrier may get two phases ahead of a warp that waits on it)
-                uint8_t* tile = sm + (L::kRing ? L::buf(c, 2, kOut).off : L::OFF_OUT) + lr * 128;
+                uint8_t* tile = sm + (L::kRing ? L::buf(c, 2).off : L::OFF_OUT) + lr * 128;
                 if (c > 0) {
                     ok = wait_warp(&bars->stored, (c - 1) & 1);
                     if (!ok) break;
@@ -778,7 +784,7 @@ cudaError_t role_maps(const ScanRole& r, const ScanPlan& p, CUtensorMap* m) {
 template <int KP, int VP, bool kOut, int kPieces>
 cudaError_t launch(const TcParams& p, cudaStream_t st) {
     auto kernel = scan_tc_kernel<KP, VP, kOut, kPieces>;
-    constexpr size_t smem = Layout<KP, VP, kPieces>::kBytes;
+    constexpr size_t smem = Layout<KP, VP, kOut, kPieces>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)p.s.plan.items, kThreads, smem, st>>>(p);
