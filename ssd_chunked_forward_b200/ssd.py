@@ -530,78 +530,113 @@ def backward(x, a, Bm, Cm, D, dy, chunk=256, *, dfinal=None, initial_state=None,
 # ---- linear attention with a decay for each head, and layer norm -------------
 #
 # These calls run on the device of their tensors, on its current torch stream
-# unless another is given.
+# unless another is given.  A single token's step takes a few microseconds on the
+# GPU, so the host's part is kept short: what follows from the tensors' shapes and
+# strides alone is checked and laid out once for each combination of them.
 
 def _on_device(name, t, device, dtype=None, shape=None, contiguous=True):
-    if not t.is_cuda or t.device != device:
+    if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {str(dtype).replace('torch.', '')}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _dtype_code(t):
-    if t.dtype == torch.bfloat16:
+def _dtype_code(dtype):
+    if dtype == torch.bfloat16:
         return SSD_DTYPE_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return SSD_DTYPE_F32
     raise ValueError("tensors must be float32 or bfloat16")
 
 
-def _stream_of(stream, device):
+def _call(where, device, stream, fn, *args):
+    """fn(*args, stream) with `device` current; raises SSDError."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return _stream(stream)
-
-
-def _linear_args(q, k, v, decay, cu_seqlens, step=False):
-    """The shape and the strides of q, k, v after their checks."""
-    lead = 1 if step or cu_seqlens is not None else 2
-    if q.dim() != lead + 2 or k.dim() != lead + 2 or v.dim() != lead + 2:
-        raise ValueError(f"q, k, v must have {lead + 2} dimensions")
-    dt = _dtype_code(q)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _on_device(name, t, q.device, q.dtype, contiguous=False)
-        if t.numel() == 0:
-            raise ValueError(f"{name} is empty")
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"the last dimension of {name} must be contiguous")
-    rows, H, K = tuple(q.shape[:lead]), q.shape[-2], q.shape[-1]
-    G, V = k.shape[-2], v.shape[-1]
-    if tuple(k.shape) != rows + (G, K) or tuple(v.shape) != rows + (G, V) or H % G:
-        raise ValueError("k must be [..., G, K] and v [..., G, V] with q's leading dimensions and G dividing H")
-    _on_device("decay", decay, q.device, torch.float32, (H,))
-    if cu_seqlens is not None:
-        _on_device("cu_seqlens", cu_seqlens, q.device, torch.int32)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-            raise ValueError("cu_seqlens must be [sequences + 1]")
-        B, T, packed = cu_seqlens.numel() - 1, rows[0], 1
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
     else:
-        B, T, packed = (rows[0], 1, 0) if step else (rows[0], rows[1], 0)
-    strides = []
-    for t in (q, k, v):
-        s = t.stride()
-        batch = 0 if packed else s[0]
-        strides.append(Strides(batch, 0 if step else s[lead - 1], s[-2]))
-    return LinearShape(B, T, H, G, K, V, dt, packed), strides, rows
+        stream = _stream(stream)
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, stream)
+    if code != SSD_OK:
+        raise SSDError(code, where)
 
 
-def _qkv(q, k, v, strides):
-    return [x for t, s in zip((q, k, v), strides) for x in (_ptr(t), ctypes.byref(s))]
+_PLANS_MOST = 4096
+_plans = {}  # shapes, strides and types -> what is laid out for them
 
 
-def _state_arg(name, t, shape, device):
-    if t is not None:
-        _on_device(name, t, device, torch.float32, (shape.B, shape.H, shape.K, shape.V))
-    return t
+def _plan(key, make):
+    plan = _plans.get(key)
+    if plan is None:
+        plan = make()
+        if len(_plans) >= _PLANS_MOST:
+            _plans.clear()
+        _plans[key] = plan
+    return plan
 
 
-def _workspace_arg(workspace, need, device, where):
-    if need == 0:
-        raise SSDError(SSD_ERR_INVALID_ARG, where)
+class _LinearPlan:
+    """What the shapes and strides of q, k, v say."""
+
+    def __init__(self, q, k, v, seqs, step):
+        lead = 1 if step or seqs is not None else 2
+        if q.dim() != lead + 2 or k.dim() != lead + 2 or v.dim() != lead + 2:
+            raise ValueError(f"q, k, v must have {lead + 2} dimensions")
+        dt = _dtype_code(q.dtype)
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            if t.numel() == 0:
+                raise ValueError(f"{name} is empty")
+            if t.shape[-1] > 1 and t.stride(-1) != 1:
+                raise ValueError(f"the last dimension of {name} must be contiguous")
+        rows, H, K = tuple(q.shape[:lead]), q.shape[-2], q.shape[-1]
+        G, V = k.shape[-2], v.shape[-1]
+        if tuple(k.shape) != rows + (G, K) or tuple(v.shape) != rows + (G, V) or H % G:
+            raise ValueError("k must be [..., G, K] and v [..., G, V] with q's leading dimensions and G dividing H")
+        if seqs is not None:
+            if len(seqs) != 1 or seqs[0] < 2:
+                raise ValueError("cu_seqlens must be [sequences + 1]")
+            B, T, packed = seqs[0] - 1, rows[0], 1
+        else:
+            B, T, packed = (rows[0], 1, 0) if step else (rows[0], rows[1], 0)
+        self.keep = [LinearShape(B, T, H, G, K, V, dt, packed)]
+        for t in (q, k, v):
+            st = t.stride()
+            self.keep.append(Strides(0 if packed else st[0], 0 if step else st[lead - 1], st[-2]))
+        self.shape = self.keep[0]
+        self.refs = [ctypes.byref(x) for x in self.keep]
+        self.H, self.y, self.k, self.v = (H,), rows + (H, V), rows + (G, K), rows + (G, V)
+        self.state = (B, H, K, V)
+        self.scale = float(K) ** -0.5
+        self.forward_bytes = linear_workspace_size(self.shape)
+        self.backward_bytes = linear_backward_workspace_size(self.shape)
+        if self.forward_bytes == 0:
+            raise SSDError(SSD_ERR_INVALID_ARG, "ssd_linear_workspace_size")
+
+
+def _linear_plan(q, k, v, decay, cu_seqlens, step=False):
+    dev, dt = q.device, q.dtype
+    seqs = None if cu_seqlens is None else cu_seqlens.shape
+    plan = _plan((q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(), dt, seqs, step),
+                 lambda: _LinearPlan(q, k, v, seqs, step))
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.device != dev or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+        if t.dtype != dt:
+            raise ValueError("q, k, v must share their type")
+    _on_device("decay", decay, dev, torch.float32, plan.H)
+    if cu_seqlens is not None:
+        _on_device("cu_seqlens", cu_seqlens, dev, torch.int32)
+    return plan
+
+
+def _workspace_arg(workspace, need, device):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
     _on_device("workspace", workspace, device, torch.uint8)
@@ -629,21 +664,23 @@ def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqle
     [S,H,K,V]; rows of a given y outside every sequence stay as they are.
     Returns y [B,T,H,V] and the state [B,H,K,V] float32 (None with
     want_final=False).  Asynchronous on the current stream of q's device."""
-    shape, strides, rows = _linear_args(q, k, v, decay, cu_seqlens)
-    dev = q.device
-    _state_arg("initial_state", initial_state, shape, dev)
+    plan, dev = _linear_plan(q, k, v, decay, cu_seqlens), q.device
+    if initial_state is not None:
+        _on_device("initial_state", initial_state, dev, torch.float32, plan.state)
     if y is None:
-        y = torch.empty(rows + (shape.H, shape.V), dtype=q.dtype, device=dev)
-    _on_device("y", y, dev, q.dtype, rows + (shape.H, shape.V))
-    if final_state is None and want_final:
-        final_state = torch.empty((shape.B, shape.H, shape.K, shape.V), dtype=torch.float32, device=dev)
-    _state_arg("final_state", final_state, shape, dev)
-    workspace = _workspace_arg(workspace, linear_workspace_size(shape), dev, "ssd_linear_workspace_size")
-    with torch.cuda.device(dev):
-        _check(load().ssd_linear_attention(
-            ctypes.byref(shape), *_qkv(q, k, v, strides), _ptr(decay), _ptr(cu_seqlens), _ptr(initial_state),
-            float(shape.K ** -0.5 if scale is None else scale), _ptr(y), _ptr(final_state), _ptr(workspace),
-            workspace.numel(), _stream_of(stream, dev)), "ssd_linear_attention")
+        y = torch.empty(plan.y, dtype=q.dtype, device=dev)
+    else:
+        _on_device("y", y, dev, q.dtype, plan.y)
+    if final_state is not None:
+        _on_device("final_state", final_state, dev, torch.float32, plan.state)
+    elif want_final:
+        final_state = torch.empty(plan.state, dtype=torch.float32, device=dev)
+    workspace = _workspace_arg(workspace, plan.forward_bytes, dev)
+    shape, sq, sk, sv = plan.refs
+    _call("ssd_linear_attention", dev, stream, load().ssd_linear_attention, shape, q.data_ptr(), sq, k.data_ptr(), sk,
+          v.data_ptr(), sv, decay.data_ptr(), _ptr(cu_seqlens), _ptr(initial_state),
+          plan.scale if scale is None else scale, y.data_ptr(), _ptr(final_state), workspace.data_ptr(),
+          workspace.numel())
     return y, final_state
 
 
@@ -651,17 +688,16 @@ def linear_attention_step(q, k, v, decay, state, *, scale=None, y=None, stream=N
     """One token of linear_attention() for a batch of sequences, in place on
     ``state`` [B,H,K,V] float32: q [B,H,K], k [B,G,K], v [B,G,V], decay [H].
     Returns y [B,H,V]."""
-    shape, strides, rows = _linear_args(q, k, v, decay, None, step=True)
-    dev = q.device
-    _state_arg("state", state, shape, dev)
+    plan, dev = _linear_plan(q, k, v, decay, None, True), q.device
+    _on_device("state", state, dev, torch.float32, plan.state)
     if y is None:
-        y = torch.empty(rows + (shape.H, shape.V), dtype=q.dtype, device=dev)
-    _on_device("y", y, dev, q.dtype, rows + (shape.H, shape.V))
-    with torch.cuda.device(dev):
-        _check(load().ssd_linear_attention_step(
-            ctypes.byref(shape), *_qkv(q, k, v, strides), _ptr(decay),
-            float(shape.K ** -0.5 if scale is None else scale), _ptr(state), _ptr(y), _stream_of(stream, dev)),
-            "ssd_linear_attention_step")
+        y = torch.empty(plan.y, dtype=q.dtype, device=dev)
+    else:
+        _on_device("y", y, dev, q.dtype, plan.y)
+    shape, sq, sk, sv = plan.refs
+    _call("ssd_linear_attention_step", dev, stream, load().ssd_linear_attention_step, shape, q.data_ptr(), sq,
+          k.data_ptr(), sk, v.data_ptr(), sv, decay.data_ptr(), plan.scale if scale is None else scale,
+          state.data_ptr(), y.data_ptr())
     return y
 
 
@@ -672,40 +708,30 @@ def linear_attention_backward(q, k, v, decay, dy, *, scale=None, initial_state=N
     dv summed over the query heads of their group) and dinit ([B,H,K,V]
     float32, or None).  dy like y; dfinal like the final state, or None.  The
     decay has no gradient.  Rows outside every packed sequence come back zero."""
-    shape, strides, rows = _linear_args(q, k, v, decay, cu_seqlens)
-    dev = q.device
-    _on_device("dy", dy, dev, q.dtype, rows + (shape.H, shape.V))
-    _state_arg("initial_state", initial_state, shape, dev)
-    _state_arg("dfinal", dfinal, shape, dev)
+    plan, dev = _linear_plan(q, k, v, decay, cu_seqlens), q.device
+    _on_device("dy", dy, dev, q.dtype, plan.y)
+    for name, t in (("initial_state", initial_state), ("dfinal", dfinal)):
+        if t is not None:
+            _on_device(name, t, dev, torch.float32, plan.state)
     new = torch.empty if cu_seqlens is None else torch.zeros
-    out = {
-        "dq": new(rows + (shape.H, shape.K), dtype=q.dtype, device=dev),
-        "dk": new(rows + (shape.G, shape.K), dtype=q.dtype, device=dev),
-        "dv": new(rows + (shape.G, shape.V), dtype=q.dtype, device=dev),
-        "dinit": (torch.empty((shape.B, shape.H, shape.K, shape.V), dtype=torch.float32, device=dev)
-                  if want_dinit else None),
-    }
-    workspace = _workspace_arg(workspace, linear_backward_workspace_size(shape), dev,
-                               "ssd_linear_backward_workspace_size")
-    with torch.cuda.device(dev):
-        _check(load().ssd_linear_attention_backward(
-            ctypes.byref(shape), *_qkv(q, k, v, strides), _ptr(decay), _ptr(cu_seqlens), _ptr(initial_state),
-            float(shape.K ** -0.5 if scale is None else scale), _ptr(dy), _ptr(dfinal), _ptr(out["dq"]),
-            _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dinit"]), _ptr(workspace), workspace.numel(),
-            _stream_of(stream, dev)), "ssd_linear_attention_backward")
-    return out
+    dq, dk, dv = (new(d, dtype=q.dtype, device=dev) for d in (q.shape, plan.k, plan.v))
+    dinit = torch.empty(plan.state, dtype=torch.float32, device=dev) if want_dinit else None
+    workspace = _workspace_arg(workspace, plan.backward_bytes, dev)
+    shape, sq, sk, sv = plan.refs
+    _call("ssd_linear_attention_backward", dev, stream, load().ssd_linear_attention_backward, shape, q.data_ptr(), sq,
+          k.data_ptr(), sk, v.data_ptr(), sv, decay.data_ptr(), _ptr(cu_seqlens), _ptr(initial_state),
+          plan.scale if scale is None else scale, dy.data_ptr(), _ptr(dfinal), dq.data_ptr(), dk.data_ptr(),
+          dv.data_ptr(), _ptr(dinit), workspace.data_ptr(), workspace.numel())
+    return {"dq": dq, "dk": dk, "dv": dv, "dinit": dinit}
 
 
-def _norm_rows(name, t, like=None):
-    """t as rows: (row stride in elements); its leading dimensions must be one."""
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError(f"{name} must have x's shape and dtype")
+def _row_stride(name, t):
+    """Elements from row to row of t, whose leading dimensions must flatten to rows."""
     if t.dim() == 0 or t.numel() == 0:
         raise ValueError(f"{name} is empty")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    stride = None  # of the flattened rows
-    want = None
+    stride = want = None
     for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
             continue
@@ -717,20 +743,44 @@ def _norm_rows(name, t, like=None):
     return t.shape[-1] if stride is None else stride
 
 
-def _norm_args(x, weight, bias, groups, gate):
-    _on_device("x", x, x.device, contiguous=False)
-    x_stride = _norm_rows("x", x)
-    width = x.shape[-1]
-    if int(groups) < 1 or width % int(groups):
-        raise ValueError("groups must divide x's last dimension")
-    for name, t in (("weight", weight), ("bias", bias)):
+class _NormPlan:
+    """What the shapes and strides of x (gate, dy) say."""
+
+    def __init__(self, x, groups, gate, dy):
+        self.x_stride = _row_stride("x", x)
+        for name, t in (("gate", gate), ("dy", dy)):
+            if t is not None and t.shape != x.shape:
+                raise ValueError(f"{name} must have x's shape and dtype")
+        self.gate_stride = 0 if gate is None else _row_stride("gate", gate)
+        self.dy_stride = 0 if dy is None else _row_stride("dy", dy)
+        width = x.shape[-1]
+        if groups < 1 or width % groups:
+            raise ValueError("groups must divide x's last dimension")
+        self.keep = NormShape(x.numel() // width, width, groups, _dtype_code(x.dtype))
+        self.shape = ctypes.byref(self.keep)
+        self.width = (width,)
+        self.stats = (x.numel() // width, groups, 2)
+        self.sums_bytes = int(load().ssd_layer_norm_backward_workspace_size(self.shape))
+
+
+def _norm_plan(x, weight, bias, groups, gate, dy=None):
+    dev, dt = x.device, x.dtype
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    for name, t in (("gate", gate), ("dy", dy)):
         if t is not None:
-            _on_device(name, t, x.device, torch.float32, (width,))
-    gate_stride = 0
-    if gate is not None:
-        _on_device("gate", gate, x.device, contiguous=False)
-        gate_stride = _norm_rows("gate", gate, x)
-    return NormShape(x.numel() // width, width, int(groups), _dtype_code(x)), x_stride, gate_stride
+            if t.device != dev:
+                raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+            if t.dtype != dt:
+                raise ValueError(f"{name} must have x's shape and dtype")
+    lay = lambda t: None if t is None else (t.shape, t.stride())  # noqa: E731
+    groups = int(groups)
+    plan = _plan((x.shape, x.stride(), dt, groups, lay(gate), lay(dy)), lambda: _NormPlan(x, groups, gate, dy))
+    if weight is not None:
+        _on_device("weight", weight, dev, torch.float32, plan.width)
+    if bias is not None:
+        _on_device("bias", bias, dev, torch.float32, plan.width)
+    return plan
 
 
 def layer_norm(x, weight=None, bias=None, *, groups=1, gate=None, eps=1e-5, y=None, stream=None):
@@ -742,15 +792,14 @@ def layer_norm(x, weight=None, bias=None, *, groups=1, gate=None, eps=1e-5, y=No
     the last contiguous), gate the same or None, weight and bias [D] float32 or
     None.  Returns y and stats [rows, groups, 2] float32 (mean and rstd, for
     layer_norm_backward)."""
-    shape, xs, gs = _norm_args(x, weight, bias, groups, gate)
+    plan, dev = _norm_plan(x, weight, bias, groups, gate), x.device
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _on_device("y", y, x.device, x.dtype, x.shape)
-    stats = torch.empty((shape.rows, shape.groups, 2), dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
-        _check(load().ssd_layer_norm(ctypes.byref(shape), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(gate), gs,
-                                     float(eps), _ptr(y), _ptr(stats), _stream_of(stream, x.device)),
-               "ssd_layer_norm")
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _on_device("y", y, dev, x.dtype, x.shape)
+    stats = torch.empty(plan.stats, dtype=torch.float32, device=dev)
+    _call("ssd_layer_norm", dev, stream, load().ssd_layer_norm, plan.shape, x.data_ptr(), plan.x_stride, _ptr(weight),
+          _ptr(bias), _ptr(gate), plan.gate_stride, eps, y.data_ptr(), stats.data_ptr())
     return y, stats
 
 
@@ -759,24 +808,16 @@ def layer_norm_backward(x, weight, bias, dy, stats, *, groups=1, gate=None, want
     """Gradients of sum(dy * y) of layer_norm() for the same inputs and its
     stats: a dict of dx, dgate (None without a gate), dweight and dbias ([D]
     float32, or None)."""
-    shape, xs, gs = _norm_args(x, weight, bias, groups, gate)
-    dev = x.device
-    _on_device("dy", dy, dev, contiguous=False)
-    ds = _norm_rows("dy", dy, x)
-    _on_device("stats", stats, dev, torch.float32, (shape.rows, shape.groups, 2))
-    new = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device=dev)  # noqa: E731
-    out = {
-        "dx": new(*x.shape, dtype=x.dtype),
-        "dgate": new(*x.shape, dtype=x.dtype) if gate is not None else None,
-        "dweight": new(shape.width) if want_dweight else None,
-        "dbias": new(shape.width) if want_dbias else None,
-    }
+    plan, dev = _norm_plan(x, weight, bias, groups, gate, dy), x.device
+    _on_device("stats", stats, dev, torch.float32, plan.stats)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dgate = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dweight = torch.empty(plan.width, dtype=torch.float32, device=dev) if want_dweight else None
+    dbias = torch.empty(plan.width, dtype=torch.float32, device=dev) if want_dbias else None
     if want_dweight or want_dbias:
-        workspace = _workspace_arg(workspace, int(load().ssd_layer_norm_backward_workspace_size(ctypes.byref(shape))),
-                                   dev, "ssd_layer_norm_backward_workspace_size")
-    with torch.cuda.device(dev):
-        _check(load().ssd_layer_norm_backward(
-            ctypes.byref(shape), _ptr(x), xs, _ptr(weight), _ptr(bias), _ptr(gate), gs, _ptr(dy), ds, _ptr(stats),
-            _ptr(out["dx"]), _ptr(out["dweight"]), _ptr(out["dbias"]), _ptr(out["dgate"]), _ptr(workspace),
-            workspace.numel() if workspace is not None else 0, _stream_of(stream, dev)), "ssd_layer_norm_backward")
-    return out
+        workspace = _workspace_arg(workspace, plan.sums_bytes, dev)
+    _call("ssd_layer_norm_backward", dev, stream, load().ssd_layer_norm_backward, plan.shape, x.data_ptr(),
+          plan.x_stride, _ptr(weight), _ptr(bias), _ptr(gate), plan.gate_stride, dy.data_ptr(), plan.dy_stride,
+          stats.data_ptr(), dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(dgate), _ptr(workspace),
+          0 if workspace is None else workspace.numel())
+    return {"dx": dx, "dgate": dgate, "dweight": dweight, "dbias": dbias}
