@@ -13,11 +13,20 @@
 // over all the rows of its block: weight and bias are loaded once, and the
 // sums of dw and db stay in its registers; a block's sums are one row of
 // `part`, and a second kernel adds those rows up in a fixed order, so the
-// result does not depend on which block ran when.  The next row's loads are
-// issued before the present row's reductions.
+// result does not depend on which block ran when.
+//
+// The rows ahead are on their way into shared memory (cp.async, each thread the
+// elements that it will read itself, so no barrier is needed) while a row is
+// worked on: four rows of 16 bytes per thread and tensor, where one row in
+// registers left the loads' latency in the open (32768 x 5120, 80 parts, gate:
+// MEASURED_FWD).  Elements of 2 bytes, which cp.async cannot copy, are
+// prefetched one row ahead in registers.
+#include <type_traits>
+
 #include "../common.cuh"
 #include "../debug_checks.cuh"
 #include "../linear.h"
+#include "../tc_common.cuh"
 
 namespace ssd {
 namespace {
@@ -50,6 +59,96 @@ struct Vec {
     }
 };
 
+// Two fp32 numbers in one instruction: the kernels issue close to one instruction a
+// cycle, and pairs halve the arithmetic's share (each number is rounded as ever).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
+}
+// VEC numbers as pairs (one number: a pair whose second half is 0)
+template <int VEC>
+struct Pairs {
+    static constexpr int N = (VEC + 1) / 2;
+    float2 p[N];
+    __device__ __forceinline__ void set(const float (&f)[VEC]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = make_float2(f[2 * i], 2 * i + 1 < VEC ? f[(2 * i + 1) % VEC] : 0.f);
+    }
+    __device__ __forceinline__ void out(float (&f)[VEC]) const {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = i & 1 ? p[i / 2].y : p[i / 2].x;
+    }
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// rows ahead, by the vectors that a thread has of each: 196 KB at most
+__host__ __device__ constexpr int norm_depth(int nv) { return nv == 1 ? 4 : nv == 2 ? 2 : 1; }
+
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, std::integral_constant<int, 16>) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, std::integral_constant<int, 8>) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, std::integral_constant<int, 4>) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A thread's elements of NT tensors in the rows ahead.  Slots are the thread's own.
+template <typename T, int VEC, int NV, int NT>
+struct Ahead {
+    static constexpr int kBytes = VEC * (int)sizeof(T);
+    static constexpr bool kRing = kBytes >= 4;
+    static constexpr int kDepth = kRing ? norm_depth(NV) : 1;
+    using V = Vec<T, VEC>;
+    V held[kRing ? 1 : NT][kRing ? 1 : NV];
+    uint8_t* mine;
+    int pitch;
+    // bytes of shared memory for a block of that many threads
+    static size_t bytes(int threads) { return kRing ? (size_t)kDepth * NT * NV * threads * kBytes : 0; }
+    __device__ __forceinline__ Ahead(uint8_t* smem) : mine(smem + threadIdx.x * kBytes), pitch(blockDim.x * kBytes) {}
+    __device__ __forceinline__ uint8_t* slot(int stage, int t, int v) const {
+        return mine + ((stage * NT + t) * NV + v) * pitch;
+    }
+    // src: the element's address, read only if `on`; else zeros come out
+    __device__ __forceinline__ void issue(int stage, int t, int v, const T* src, bool on) {
+        if constexpr (kRing) {
+            if (on) {
+                cp_async(static_cast<uint32_t>(__cvta_generic_to_shared(slot(stage, t, v))), src,
+                         std::integral_constant<int, kBytes>());
+            } else {
+                V none;
+                none.clear();
+                *reinterpret_cast<typename V::Raw*>(slot(stage, t, v)) = none.raw;
+            }
+        } else {
+            held[t][v].clear();
+            if (on) held[t][v].load(src);
+        }
+    }
+    __device__ __forceinline__ void commit() {
+        if constexpr (kRing) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // the oldest row of kDepth is here
+    __device__ __forceinline__ void wait() {
+        if constexpr (kRing) asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    }
+    __device__ __forceinline__ void get(int stage, int t, int v, Pairs<VEC>& to) const {
+        float f[VEC];
+        if constexpr (kRing) {
+            V x;
+            x.load(reinterpret_cast<const T*>(slot(stage, t, v)));
+            x.get(f);
+        } else {
+            held[t][v].get(f);
+        }
+        to.set(f);
+    }
+};
+
 // 1 / (1 + exp(-z)).  bf16 results take the special-function forms (relative
 // error below 2^-20, against the result's 2^-9); fp32 results the exact ones.
 template <typename T> __device__ __forceinline__ float sigmoid(float z);
@@ -70,246 +169,283 @@ struct NormShape {
     int slabs;   // blocks across a row
     int parts;   // blocks down the rows
     int threads;
+    int ring_bytes;  // of the rows ahead (the backward's moments lie behind them)
 };
 
-// Sum of a and b over the team, in every thread of it.  Teams wider than a warp
-// are the whole block; `turn` alternates the buffer so that one barrier per sum
-// is enough.
-__device__ __forceinline__ void team_sum(float& a, float& b, int team, int turn, float (*buf)[2][32]) {
+// Sums of N numbers over the team, in every thread of it.  Teams wider than a warp
+// are the whole block; `turn` alternates the buffer so that one barrier per sum is
+// enough.
+template <int N>
+__device__ __forceinline__ void team_sum(float (&a)[N], int team, int turn, float (*buf)[2][32]) {
     const int w = team < 32 ? team : 32;
     for (int o = w >> 1; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
     }
     if (team > 32) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
         if (lane == 0) {
-            buf[turn][0][warp] = a;
-            buf[turn][1][warp] = b;
+#pragma unroll
+            for (int i = 0; i < N; ++i) buf[turn][i][warp] = a[i];
         }
         __syncthreads();
-        a = lane < nw ? buf[turn][0][lane] : 0.f;
-        b = lane < nw ? buf[turn][1][lane] : 0.f;
+        // four warps' sums to a read (the unused ones stay zero)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
+        for (int i = 0; i < N; ++i) a[i] = 0.f;
+        for (int k = 0; k < nw; k += 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float4 f = *reinterpret_cast<const float4*>(&buf[turn][i][k]);
+                a[i] += (f.x + f.y) + (f.z + f.w);
+            }
         }
     }
 }
 
+// A thread's place: its part of the row, its columns, and weight and bias there.
+template <int VEC, int NV>
+struct Place {
+    int lane, slot, group, col[NV];
+    bool on, in[NV];
+    Pairs<VEC> w[NV], b[NV];
+    __device__ __forceinline__ Place(const NormArgs& a, const NormShape& s, int slab, bool bias) {
+        const int tid = threadIdx.x, tm = tid / s.team;
+        lane = tid % s.team;
+        slot = tm / s.gpb;
+        on = slot < s.slots;
+        group = slab * s.gpb + tm - slot * s.gpb;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (lane + v * s.team) * VEC;
+            in[v] = on && c < s.n;
+            col[v] = group * s.n + c;
+            float fw[VEC], fb[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                fw[i] = a.weight && in[v] && SSD_INB(col[v] + i, a.width) ? a.weight[col[v] + i] : 1.f;
+                fb[i] = bias && a.bias && in[v] && SSD_INB(col[v] + i, a.width) ? a.bias[col[v] + i] : 0.f;
+            }
+            w[v].set(fw);
+            b[v].set(fb);
+        }
+    }
+};
+
 template <typename T, int VEC, int NV, bool GATE>
-__global__ void __launch_bounds__(norm_threads(VEC, NV))
+__global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 2 : 1)
     layer_norm_kernel(const NormArgs a, const NormShape s) {
-    __shared__ float buf[2][2][32];
+    __shared__ __align__(16) float buf[2][2][32];
+    extern __shared__ __align__(16) uint8_t ring[];
+    constexpr int P = Pairs<VEC>::N;
     const int slab = blockIdx.x % s.slabs, part = blockIdx.x / s.slabs;
-    const int tid = threadIdx.x, lane = tid % s.team, tm = tid / s.team;
-    const int slot = tm / s.gpb, gl = tm - slot * s.gpb;
-    const bool on = slot < s.slots;
-    const int group = slab * s.gpb + gl;
+    const Place<VEC, NV> at(a, s, slab, true);
+    for (int i = threadIdx.x; i < 128; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+    __syncthreads();
     const float inv_n = 1.f / (float)s.n;
-    float w[NV][VEC], b[NV][VEC];
-    int col[NV];
-    bool in[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int c = (lane + v * s.team) * VEC;
-        in[v] = on && c < s.n;
-        col[v] = group * s.n + c;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            w[v][i] = a.weight && in[v] && SSD_INB(col[v] + i, a.width) ? a.weight[col[v] + i] : 1.f;
-            b[v][i] = a.bias && in[v] && SSD_INB(col[v] + i, a.width) ? a.bias[col[v] + i] : 0.f;
-        }
-    }
-    Vec<T, VEC> xr[NV], zr[NV];
+    Ahead<T, VEC, NV, GATE ? 2 : 1> rows(ring);
     const long long step = (long long)s.parts * s.slots;
-    auto fetch = [&](long long row) {
+    auto fetch = [&](long long row, int stage) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            xr[v].clear();
-            if (GATE) zr[v].clear();
-            if (in[v] && row < a.rows && SSD_INB(col[v] + VEC - 1, a.width)) {
-                xr[v].load((const T*)a.x + row * a.x_stride + col[v]);
-                if (GATE) zr[v].load((const T*)a.gate + row * a.gate_stride + col[v]);
-            }
+            const bool use = at.in[v] && row < a.rows && SSD_INB(at.col[v] + VEC - 1, a.width);
+            rows.issue(stage, 0, v, (const T*)a.x + row * a.x_stride + at.col[v], use);
+            if (GATE) rows.issue(stage, 1, v, (const T*)a.gate + row * a.gate_stride + at.col[v], use);
         }
+        rows.commit();
     };
-    int turn = 0;
+    int turn = 0, stage = 0;
     long long base = (long long)part * s.slots;
-    fetch(base + slot);
+    for (int i = 0; i < rows.kDepth; ++i) fetch(base + at.slot + i * step, i);
     for (; base < a.rows; base += step) {
-        const long long row = base + slot;
-        float x[NV][VEC], z[NV][VEC];
+        const long long row = base + at.slot;
+        Pairs<VEC> x[NV], z[NV];
+        rows.wait();
+        float2 sum2 = both(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            xr[v].get(x[v]);
-            if (GATE) zr[v].get(z[v]);
+            rows.get(stage, 0, v, x[v]);
+            if (GATE) rows.get(stage, 1, v, z[v]);
+#pragma unroll
+            for (int i = 0; i < P; ++i) sum2 = add2(sum2, x[v].p[i]);  // (zeros behind the part)
         }
-        fetch(row + step);
-        float sum = 0.f, sq = 0.f, none = 0.f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) sum += x[v][i];
-        team_sum(sum, none, s.team, turn, buf);
+        fetch(row + rows.kDepth * step, stage);
+        stage = stage + 1 == rows.kDepth ? 0 : stage + 1;
+        float sum[1] = {sum2.x + sum2.y};
+        team_sum(sum, s.team, turn, buf);
         turn ^= 1;
-        const float mean = sum * inv_n;
+        const float mean = sum[0] * inv_n;
+        float2 sq2 = both(0.f);
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v) {
+            const float2 away = both(at.in[v] ? -mean : 0.f);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                x[v][i] = in[v] ? x[v][i] - mean : 0.f;
-                sq = fmaf(x[v][i], x[v][i], sq);
+            for (int i = 0; i < P; ++i) {
+                x[v].p[i] = add2(x[v].p[i], away);
+                if (VEC == 1) x[v].p[i].y = 0.f;
+                sq2 = tc::fma2(x[v].p[i], x[v].p[i], sq2);
             }
-        team_sum(sq, none, s.team, turn, buf);
+        }
+        float sq[1] = {sq2.x + sq2.y};
+        team_sum(sq, s.team, turn, buf);
         turn ^= 1;
-        const float rstd = 1.f / sqrtf(fmaf(sq, inv_n, a.eps));
-        if (row < a.rows && on) {
-            if (a.stats && lane == 0) {
-                const long long at = (row * a.groups + group) * 2;
-                if (SSD_INB(at + 1, a.rows * a.groups * 2)) {
-                    a.stats[at] = mean;
-                    a.stats[at + 1] = rstd;
-                }
+        const float rstd = 1.f / sqrtf(fmaf(sq[0], inv_n, a.eps));
+        if (row < a.rows && at.on) {
+            if (a.stats && at.lane == 0) {
+                const long long to = (row * a.groups + at.group) * 2;
+                if (SSD_INB(to + 1, a.rows * a.groups * 2)) *reinterpret_cast<float2*>(a.stats + to) = make_float2(mean, rstd);
             }
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                if (!in[v] || !SSD_INB(row * a.width + col[v] + VEC - 1, a.rows * a.width)) continue;
-                float y[VEC];
+                if (!at.in[v] || !SSD_INB(row * a.width + at.col[v] + VEC - 1, a.rows * a.width)) continue;
+                Pairs<VEC> y;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    y[i] = fmaf(x[v][i] * rstd, w[v][i], b[v][i]);
-                    if (GATE) y[i] *= z[v][i] * sigmoid<T>(z[v][i]);
+                for (int i = 0; i < P; ++i) {
+                    y.p[i] = tc::fma2(tc::mul2(x[v].p[i], both(rstd)), at.w[v].p[i], at.b[v].p[i]);
+                    if (GATE) {
+                        const float2 sg = make_float2(sigmoid<T>(z[v].p[i].x), sigmoid<T>(z[v].p[i].y));
+                        y.p[i] = tc::mul2(y.p[i], tc::mul2(z[v].p[i], sg));
+                    }
                 }
-                Vec<T, VEC>::store((T*)a.y + row * a.width + col[v], y);
+                float f[VEC];
+                y.out(f);
+                Vec<T, VEC>::store((T*)a.y + row * a.width + at.col[v], f);
             }
         }
     }
 }
 
 template <typename T, int VEC, int NV, bool GATE>
-__global__ void __launch_bounds__(norm_threads(VEC, NV))
+__global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 2 : 1)
     layer_norm_backward_kernel(const NormArgs a, const NormShape s) {
-    extern __shared__ float sums[];  // [slots][cols of the block][2], when slots > 1
-    __shared__ float buf[2][2][32];
+    extern __shared__ __align__(16) uint8_t ring[];
+    float* sums = reinterpret_cast<float*>(ring);  // at the end: [slots][2][cols of the block], when slots > 1
+    __shared__ __align__(16) float buf[2][2][32];
+    constexpr int P = Pairs<VEC>::N, NT = GATE ? 3 : 2;
     const int slab = blockIdx.x % s.slabs, part = blockIdx.x / s.slabs;
-    const int tid = threadIdx.x, lane = tid % s.team, tm = tid / s.team;
-    const int slot = tm / s.gpb, gl = tm - slot * s.gpb;
-    const bool on = slot < s.slots;
-    const int group = slab * s.gpb + gl;
+    const Place<VEC, NV> at(a, s, slab, GATE);
+    for (int i = threadIdx.x; i < 128; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+    __syncthreads();
     const float inv_n = 1.f / (float)s.n;
-    float w[NV][VEC], b[NV][VEC], dw[NV][VEC], db[NV][VEC];
-    int col[NV];
-    bool in[NV];
+    Pairs<VEC> dw[NV], db[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int c = (lane + v * s.team) * VEC;
-        in[v] = on && c < s.n;
-        col[v] = group * s.n + c;
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            w[v][i] = a.weight && in[v] && SSD_INB(col[v] + i, a.width) ? a.weight[col[v] + i] : 1.f;
-            b[v][i] = GATE && a.bias && in[v] && SSD_INB(col[v] + i, a.width) ? a.bias[col[v] + i] : 0.f;
-            dw[v][i] = db[v][i] = 0.f;
-        }
-    }
-    Vec<T, VEC> xr[NV], dr[NV], zr[NV];
-    float2 st = make_float2(0.f, 0.f);
+        for (int i = 0; i < P; ++i) dw[v].p[i] = db[v].p[i] = both(0.f);
+    Ahead<T, VEC, NV, NT> rows(ring);
+    // mean and rstd of the part go with them
+    constexpr int depth = Ahead<T, VEC, NV, NT>::kDepth;
+    float2* moments = reinterpret_cast<float2*>(ring + s.ring_bytes) + threadIdx.x;
+    float2 held = make_float2(0.f, 0.f);
     const long long step = (long long)s.parts * s.slots;
-    auto fetch = [&](long long row) {
+    auto fetch = [&](long long row, int stage) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            xr[v].clear();
-            dr[v].clear();
-            if (GATE) zr[v].clear();
-            if (in[v] && row < a.rows && SSD_INB(col[v] + VEC - 1, a.width)) {
-                xr[v].load((const T*)a.x + row * a.x_stride + col[v]);
-                dr[v].load((const T*)a.dy + row * a.dy_stride + col[v]);
-                if (GATE) zr[v].load((const T*)a.gate + row * a.gate_stride + col[v]);
-            }
+            const bool use = at.in[v] && row < a.rows && SSD_INB(at.col[v] + VEC - 1, a.width);
+            rows.issue(stage, 0, v, (const T*)a.x + row * a.x_stride + at.col[v], use);
+            rows.issue(stage, 1, v, (const T*)a.dy + row * a.dy_stride + at.col[v], use);
+            if (GATE) rows.issue(stage, 2, v, (const T*)a.gate + row * a.gate_stride + at.col[v], use);
         }
-        const long long at = row * a.groups + group;
-        if (on && row < a.rows && SSD_INB(at, a.rows * a.groups)) st = reinterpret_cast<const float2*>(a.stats)[at];
+        const long long m = row * a.groups + at.group;
+        const bool use = at.on && row < a.rows && SSD_INB(m, a.rows * a.groups);
+        if constexpr (rows.kRing) {
+            if (use)
+                cp_async(static_cast<uint32_t>(__cvta_generic_to_shared(moments + stage * blockDim.x)), a.stats + 2 * m,
+                         std::integral_constant<int, 8>());
+            else
+                moments[stage * blockDim.x] = make_float2(0.f, 0.f);
+        } else {
+            held = use ? reinterpret_cast<const float2*>(a.stats)[m] : make_float2(0.f, 0.f);
+        }
+        rows.commit();
     };
-    int turn = 0;
+    int turn = 0, stage = 0;
     long long base = (long long)part * s.slots;
-    fetch(base + slot);
+    for (int i = 0; i < depth; ++i) fetch(base + at.slot + i * step, i);
     for (; base < a.rows; base += step) {
-        const long long row = base + slot;
-        float xh[NV][VEC], dxh[NV][VEC];
-        const float mean = st.x, rstd = st.y;
-        const bool live = row < a.rows && on;
-        float s1 = 0.f, s2 = 0.f;
+        const long long row = base + at.slot;
+        const bool live = row < a.rows && at.on;
+        Pairs<VEC> xh[NV], dxh[NV];
+        rows.wait();
+        if constexpr (rows.kRing) held = moments[stage * blockDim.x];
+        const float rstd = held.y;
+        float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            float x[VEC], d[VEC], z[VEC];
-            xr[v].get(x);
-            dr[v].get(d);
-            if (GATE) zr[v].get(z);
-            const bool use = in[v] && live;
-            float dz[VEC];
+            Pairs<VEC> x, d, z, dz;
+            rows.get(stage, 0, v, x);
+            rows.get(stage, 1, v, d);
+            if (GATE) rows.get(stage, 2, v, z);
+            const float2 away = both(at.in[v] ? -held.x : 0.f);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float h = use ? (x[i] - mean) * rstd : 0.f;
-                float du = d[i];
+            for (int i = 0; i < P; ++i) {
+                // zeros behind the part and the last row: dy = 0 there, so they add nothing
+                const float2 h = tc::mul2(add2(x.p[i], away), both(rstd));
+                float2 du = d.p[i];
                 if (GATE) {
-                    const float sg = sigmoid<T>(z[i]);
-                    dz[i] = d[i] * fmaf(h, w[v][i], b[v][i]) * (sg * fmaf(z[i], 1.f - sg, 1.f));
-                    du *= z[i] * sg;
+                    const float2 sg = make_float2(sigmoid<T>(z.p[i].x), sigmoid<T>(z.p[i].y));
+                    const float2 zs = tc::mul2(z.p[i], sg);  // silu(z); silu'(z) = sg + zs (1 - sg)
+                    const float2 slope = tc::fma2(zs, add2(both(1.f), make_float2(-sg.x, -sg.y)), sg);
+                    dz.p[i] = tc::mul2(tc::mul2(du, slope), tc::fma2(h, at.w[v].p[i], at.b[v].p[i]));
+                    du = tc::mul2(du, zs);
                 }
-                du = use ? du : 0.f;
-                dw[v][i] = fmaf(du, h, dw[v][i]);
-                db[v][i] += du;
-                xh[v][i] = h;
-                dxh[v][i] = du * w[v][i];
-                s1 += dxh[v][i];
-                s2 = fmaf(dxh[v][i], h, s2);
+                dw[v].p[i] = tc::fma2(du, h, dw[v].p[i]);
+                db[v].p[i] = add2(db[v].p[i], du);
+                xh[v].p[i] = h;
+                dxh[v].p[i] = tc::mul2(du, at.w[v].p[i]);
+                s1 = add2(s1, dxh[v].p[i]);
+                s2 = tc::fma2(dxh[v].p[i], h, s2);
             }
-            if (GATE && use && SSD_INB(row * a.width + col[v] + VEC - 1, a.rows * a.width))
-                Vec<T, VEC>::store((T*)a.dgate + row * a.width + col[v], dz);
+            if (GATE && at.in[v] && live && SSD_INB(row * a.width + at.col[v] + VEC - 1, a.rows * a.width)) {
+                float f[VEC];
+                dz.out(f);
+                Vec<T, VEC>::store((T*)a.dgate + row * a.width + at.col[v], f);
+            }
         }
-        fetch(row + step);
-        team_sum(s1, s2, s.team, turn, buf);
+        fetch(row + depth * step, stage);
+        stage = stage + 1 == depth ? 0 : stage + 1;
+        float both_sums[2] = {s1.x + s1.y, s2.x + s2.y};
+        team_sum(both_sums, s.team, turn, buf);
         turn ^= 1;
-        s1 *= inv_n;
-        s2 *= inv_n;
         if (live) {
+            const float2 m1 = both(-both_sums[0] * inv_n), m2 = both(-both_sums[1] * inv_n);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                if (!in[v] || !SSD_INB(row * a.width + col[v] + VEC - 1, a.rows * a.width)) continue;
-                float dx[VEC];
+                if (!at.in[v] || !SSD_INB(row * a.width + at.col[v] + VEC - 1, a.rows * a.width)) continue;
+                Pairs<VEC> dx;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) dx[i] = rstd * (dxh[v][i] - s1 - xh[v][i] * s2);
-                Vec<T, VEC>::store((T*)a.dx + row * a.width + col[v], dx);
+                for (int i = 0; i < P; ++i)
+                    dx.p[i] = tc::mul2(both(rstd), tc::fma2(xh[v].p[i], m2, add2(dxh[v].p[i], m1)));
+                float f[VEC];
+                dx.out(f);
+                Vec<T, VEC>::store((T*)a.dx + row * a.width + at.col[v], f);
             }
         }
     }
     if (!a.part) return;
     float* pw = a.part + (size_t)part * 2 * a.width;
-    if (s.slots == 1) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (in[v] && SSD_INB(col[v] + i, a.width)) {
-                    pw[col[v] + i] = dw[v][i];
-                    pw[a.width + col[v] + i] = db[v][i];
-                }
-        return;
-    }
     const int cols = s.gpb * s.n;
+    if (s.slots > 1) __syncthreads();  // every slot of the ring has been read
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+        float fw[VEC], fb[VEC];
+        dw[v].out(fw);
+        db[v].out(fb);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            if (in[v]) {
-                const int c = col[v] + i - slab * cols;
-                sums[(slot * 2) * cols + c] = dw[v][i];
-                sums[(slot * 2 + 1) * cols + c] = db[v][i];
+        for (int i = 0; i < VEC; ++i) {
+            if (!at.in[v] || !SSD_INB(at.col[v] + i, a.width)) continue;
+            if (s.slots == 1) {
+                pw[at.col[v] + i] = fw[i];
+                pw[a.width + at.col[v] + i] = fb[i];
+            } else {
+                const int c = at.col[v] + i - slab * cols;
+                sums[(at.slot * 2) * cols + c] = fw[i];
+                sums[(at.slot * 2 + 1) * cols + c] = fb[i];
             }
+        }
+    }
+    if (s.slots == 1) return;
     __syncthreads();
-    for (int c = tid; c < 2 * cols; c += blockDim.x) {
+    for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) {
         float t = 0.f;
         for (int k = 0; k < s.slots; ++k) t += sums[k * 2 * cols + c];
         const int cc = c < cols ? c : c - cols;
@@ -390,17 +526,26 @@ int norm_vec(const NormArgs& a) {
 }
 
 template <typename T, int VEC, int NV>
-cudaError_t launch(const NormArgs& a, const NormShape& s, bool backward, cudaStream_t st) {
+cudaError_t launch(const NormArgs& a, NormShape s, bool backward, cudaStream_t st) {
     const long long grid = (long long)s.slabs * s.parts;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (!backward) {
-        if (a.gate) layer_norm_kernel<T, VEC, NV, true><<<(unsigned)grid, s.threads, 0, st>>>(a, s);
-        else layer_norm_kernel<T, VEC, NV, false><<<(unsigned)grid, s.threads, 0, st>>>(a, s);
-    } else {
-        const size_t smem = s.slots > 1 ? (size_t)s.slots * 2 * s.gpb * s.n * sizeof(float) : 0;
-        if (a.gate) layer_norm_backward_kernel<T, VEC, NV, true><<<(unsigned)grid, s.threads, smem, st>>>(a, s);
-        else layer_norm_backward_kernel<T, VEC, NV, false><<<(unsigned)grid, s.threads, smem, st>>>(a, s);
+    const int tensors = (a.gate ? 2 : 1) + (backward ? 1 : 0);
+    size_t smem = tensors == 1   ? Ahead<T, VEC, NV, 1>::bytes(s.threads)
+                  : tensors == 2 ? Ahead<T, VEC, NV, 2>::bytes(s.threads)
+                                 : Ahead<T, VEC, NV, 3>::bytes(s.threads);
+    s.ring_bytes = (int)smem;
+    if (backward) {
+        smem += (size_t)norm_depth(NV) * s.threads * sizeof(float2);
+        const size_t sums = s.slots > 1 ? (size_t)s.slots * 2 * s.gpb * s.n * sizeof(float) : 0;
+        if (smem < sums) smem = sums;
     }
+    auto kernel = backward ? (a.gate ? layer_norm_backward_kernel<T, VEC, NV, true> : layer_norm_backward_kernel<T, VEC, NV, false>)
+                           : (a.gate ? layer_norm_kernel<T, VEC, NV, true> : layer_norm_kernel<T, VEC, NV, false>);
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<(unsigned)grid, s.threads, smem, st>>>(a, s);
     return cudaGetLastError();
 }
 
