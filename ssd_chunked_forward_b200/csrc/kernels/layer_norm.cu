@@ -158,7 +158,9 @@ template <> __device__ __forceinline__ float sigmoid<__nv_bfloat16>(float z) {
 }
 
 // the most threads that norm_shape() gives a block of this variant
-constexpr int norm_threads(int vec, int nv) { return (vec == 4 && nv == 4) || nv == 16 ? 1024 : 512; }
+constexpr int norm_threads(int vec, int nv) {
+    return (vec == 4 && nv == 4) || nv == 16 ? 1024 : nv == 1 && vec > 2 ? 320 : 512;
+}
 
 // How the threads of a launch lie over rows and columns.
 struct NormShape {
@@ -170,37 +172,69 @@ struct NormShape {
     int parts;   // blocks down the rows
     int threads;
     int ring_bytes;  // of the rows ahead (the backward's moments lie behind them)
+    long long step;  // rows from one row of a thread to the next, and in numbers of each tensor
+    long long x_step, gate_step, dy_step, out_step, stats_step;
 };
 
 // Sums of N numbers over the team, in every thread of it.  Teams wider than a warp
-// are the whole block; `turn` alternates the buffer so that one barrier per sum is
-// enough.
+// are the whole block; the caller alternates between two buffers, so that one
+// barrier per sum is enough.
 template <int N>
-__device__ __forceinline__ void team_sum(float (&a)[N], int team, int turn, float (*buf)[2][32]) {
-    const int w = team < 32 ? team : 32;
-    for (int o = w >> 1; o > 0; o >>= 1) {
+__device__ __forceinline__ void team_sum(float (&a)[N], int team, float (*buf)[32]) {
+    if (team >= 32) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
+    } else {
+        for (int o = team >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) a[i] += __shfl_xor_sync(0xffffffffu, a[i], o);
     }
     if (team > 32) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-        if (lane == 0) {
+        const int nw = blockDim.x >> 5;
+        if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) buf[turn][i][warp] = a[i];
+            for (int i = 0; i < N; ++i) buf[i][threadIdx.x >> 5] = a[i];
         }
         __syncthreads();
-        // four warps' sums to a read (the unused ones stay zero)
+        // four warps' sums to a read (those of no warp stay zero)
 #pragma unroll
-        for (int i = 0; i < N; ++i) a[i] = 0.f;
-        for (int k = 0; k < nw; k += 4) {
+        for (int i = 0; i < N; ++i) {
+            const float4 f = *reinterpret_cast<const float4*>(&buf[i][0]), g = *reinterpret_cast<const float4*>(&buf[i][4]);
+            a[i] = ((f.x + f.y) + (f.z + f.w)) + ((g.x + g.y) + (g.z + g.w));
+        }
+        for (int k = 8; k < nw; k += 4) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const float4 f = *reinterpret_cast<const float4*>(&buf[turn][i][k]);
+                const float4 f = *reinterpret_cast<const float4*>(&buf[i][k]);
                 a[i] += (f.x + f.y) + (f.z + f.w);
             }
         }
     }
 }
+
+// x^(-1/2): the special-function unit's and one Newton step (within one rounding or
+// two; the division and root that round exactly are forty instructions)
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float r = rsqrtf(x);
+    return r * fmaf(-0.5f * x * r, r, 1.5f);
+}
+
+// The rows of a thread: row0, row0 + step, ..  Indices are counted in 32 bits and
+// pointers moved along: with an index product for each access a row of 8 numbers
+// cost a thread 255 instructions, now 140, and issuing them is what bounds
+// these kernels next to HBM.
+struct Rows {
+    long long row0;
+    int mine, all;  // rows of this thread, and of the block's first
+    __device__ __forceinline__ Rows(const NormArgs& a, const NormShape& s, int part, int slot, bool on) {
+        const long long first = (long long)part * s.slots;
+        row0 = first + slot;
+        all = first < a.rows ? (int)((a.rows - first + s.step - 1) / s.step) : 0;
+        mine = on && row0 < a.rows ? (int)((a.rows - row0 + s.step - 1) / s.step) : 0;
+    }
+};
 
 // A thread's place: its part of the row, its columns, and weight and bias there.
 template <int VEC, int NV>
@@ -232,49 +266,57 @@ struct Place {
 };
 
 template <typename T, int VEC, int NV, bool GATE>
-__global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 2 : 1)
+__global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 3 : 1)
     layer_norm_kernel(const NormArgs a, const NormShape s) {
-    __shared__ __align__(16) float buf[2][2][32];
-    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ __align__(16) float buf[2][1][32];
+    extern __shared__ __align__(16) uint8_t smem[];
     constexpr int P = Pairs<VEC>::N;
+    using Ring = Ahead<T, VEC, NV, GATE ? 2 : 1>;
+    constexpr int depth = Ring::kDepth;
     const int slab = blockIdx.x % s.slabs, part = blockIdx.x / s.slabs;
     const Place<VEC, NV> at(a, s, slab, true);
-    for (int i = threadIdx.x; i < 128; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
     __syncthreads();
     const float inv_n = 1.f / (float)s.n;
-    Ahead<T, VEC, NV, GATE ? 2 : 1> rows(ring);
-    const long long step = (long long)s.parts * s.slots;
-    auto fetch = [&](long long row, int stage) {
+    const Rows rows(a, s, part, at.slot, at.on);
+    Ring ring(smem);
+    const int next = s.team * VEC;  // from one vector of a thread to the next
+    const T* px = (const T*)a.x + rows.row0 * a.x_stride + at.col[0];
+    const T* pz = (const T*)a.gate + rows.row0 * a.gate_stride + at.col[0];
+    T* py = (T*)a.y + rows.row0 * a.width + at.col[0];
+    float2* pst = a.stats ? reinterpret_cast<float2*>(a.stats) + rows.row0 * a.groups + at.group : nullptr;
+    auto fetch = [&](int k, int stage) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const bool use = at.in[v] && row < a.rows && SSD_INB(at.col[v] + VEC - 1, a.width);
-            rows.issue(stage, 0, v, (const T*)a.x + row * a.x_stride + at.col[v], use);
-            if (GATE) rows.issue(stage, 1, v, (const T*)a.gate + row * a.gate_stride + at.col[v], use);
+            const bool use = at.in[v] && k < rows.mine &&
+                             SSD_INB((rows.row0 + k * s.step) * a.width + at.col[v] + VEC - 1, a.rows * a.width);
+            ring.issue(stage, 0, v, px + v * next, use);
+            if (GATE) ring.issue(stage, 1, v, pz + v * next, use);
         }
-        rows.commit();
+        px += s.x_step;
+        if (GATE) pz += s.gate_step;
+        ring.commit();
     };
-    int turn = 0, stage = 0;
-    long long base = (long long)part * s.slots;
-    for (int i = 0; i < rows.kDepth; ++i) fetch(base + at.slot + i * step, i);
-    for (; base < a.rows; base += step) {
-        const long long row = base + at.slot;
+    int stage = 0;
+#pragma unroll
+    for (int i = 0; i < depth; ++i) fetch(i, i);
+    for (int k = 0; k < rows.all; ++k) {
         Pairs<VEC> x[NV], z[NV];
-        rows.wait();
-        float2 sum2 = both(0.f);
+        ring.wait();
+        float2 t = both(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            rows.get(stage, 0, v, x[v]);
-            if (GATE) rows.get(stage, 1, v, z[v]);
+            ring.get(stage, 0, v, x[v]);
+            if (GATE) ring.get(stage, 1, v, z[v]);
 #pragma unroll
-            for (int i = 0; i < P; ++i) sum2 = add2(sum2, x[v].p[i]);  // (zeros behind the part)
+            for (int i = 0; i < P; ++i) t = add2(t, x[v].p[i]);  // (zeros behind the part)
         }
-        fetch(row + rows.kDepth * step, stage);
-        stage = stage + 1 == rows.kDepth ? 0 : stage + 1;
-        float sum[1] = {sum2.x + sum2.y};
-        team_sum(sum, s.team, turn, buf);
-        turn ^= 1;
+        fetch(k + depth, stage);
+        stage = stage + 1 == depth ? 0 : stage + 1;
+        float sum[1] = {t.x + t.y};
+        team_sum(sum, s.team, buf[0]);
         const float mean = sum[0] * inv_n;
-        float2 sq2 = both(0.f);
+        t = both(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const float2 away = both(at.in[v] ? -mean : 0.f);
@@ -282,21 +324,17 @@ __global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 2 : 1)
             for (int i = 0; i < P; ++i) {
                 x[v].p[i] = add2(x[v].p[i], away);
                 if (VEC == 1) x[v].p[i].y = 0.f;
-                sq2 = tc::fma2(x[v].p[i], x[v].p[i], sq2);
+                t = tc::fma2(x[v].p[i], x[v].p[i], t);
             }
         }
-        float sq[1] = {sq2.x + sq2.y};
-        team_sum(sq, s.team, turn, buf);
-        turn ^= 1;
-        const float rstd = 1.f / sqrtf(fmaf(sq[0], inv_n, a.eps));
-        if (row < a.rows && at.on) {
-            if (a.stats && at.lane == 0) {
-                const long long to = (row * a.groups + at.group) * 2;
-                if (SSD_INB(to + 1, a.rows * a.groups * 2)) *reinterpret_cast<float2*>(a.stats + to) = make_float2(mean, rstd);
-            }
+        float sq[1] = {t.x + t.y};
+        team_sum(sq, s.team, buf[1]);
+        const float rstd = inv_sqrt(fmaf(sq[0], inv_n, a.eps));
+        if (k < rows.mine) {
+            if (pst && at.lane == 0 && SSD_INB((float*)pst - a.stats + 1, a.rows * a.groups * 2)) *pst = make_float2(mean, rstd);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                if (!at.in[v] || !SSD_INB(row * a.width + at.col[v] + VEC - 1, a.rows * a.width)) continue;
+                if (!at.in[v] || !SSD_INB(py + v * next - (T*)a.y + VEC - 1, a.rows * a.width)) continue;
                 Pairs<VEC> y;
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
@@ -308,19 +346,23 @@ __global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 2 : 1)
                 }
                 float f[VEC];
                 y.out(f);
-                Vec<T, VEC>::store((T*)a.y + row * a.width + at.col[v], f);
+                Vec<T, VEC>::store(py + v * next, f);
             }
         }
+        py += s.out_step;
+        if (pst) pst += s.stats_step;
     }
 }
 
 template <typename T, int VEC, int NV, bool GATE>
 __global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 2 : 1)
     layer_norm_backward_kernel(const NormArgs a, const NormShape s) {
-    extern __shared__ __align__(16) uint8_t ring[];
-    float* sums = reinterpret_cast<float*>(ring);  // at the end: [slots][2][cols of the block], when slots > 1
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* sums = reinterpret_cast<float*>(smem);  // at the end: [slots][2][cols of the block], when slots > 1
     __shared__ __align__(16) float buf[2][2][32];
     constexpr int P = Pairs<VEC>::N, NT = GATE ? 3 : 2;
+    using Ring = Ahead<T, VEC, NV, NT>;
+    constexpr int depth = Ring::kDepth;
     const int slab = blockIdx.x % s.slabs, part = blockIdx.x / s.slabs;
     const Place<VEC, NV> at(a, s, slab, GATE);
     for (int i = threadIdx.x; i < 128; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
@@ -331,50 +373,58 @@ __global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 2 : 1)
     for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int i = 0; i < P; ++i) dw[v].p[i] = db[v].p[i] = both(0.f);
-    Ahead<T, VEC, NV, NT> rows(ring);
-    // mean and rstd of the part go with them
-    constexpr int depth = Ahead<T, VEC, NV, NT>::kDepth;
-    float2* moments = reinterpret_cast<float2*>(ring + s.ring_bytes) + threadIdx.x;
+    const Rows rows(a, s, part, at.slot, at.on);
+    Ring ring(smem);
+    // mean and rstd of the part go with the rows ahead
+    float2* moments = reinterpret_cast<float2*>(smem + s.ring_bytes) + threadIdx.x;
     float2 held = make_float2(0.f, 0.f);
-    const long long step = (long long)s.parts * s.slots;
-    auto fetch = [&](long long row, int stage) {
+    const int next = s.team * VEC;
+    const T* px = (const T*)a.x + rows.row0 * a.x_stride + at.col[0];
+    const T* pd = (const T*)a.dy + rows.row0 * a.dy_stride + at.col[0];
+    const T* pz = (const T*)a.gate + rows.row0 * a.gate_stride + at.col[0];
+    const float2* pst = reinterpret_cast<const float2*>(a.stats) + rows.row0 * a.groups + at.group;
+    long long to = rows.row0 * a.width + at.col[0];  // in dx and dgate
+    auto fetch = [&](int k, int stage) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const bool use = at.in[v] && row < a.rows && SSD_INB(at.col[v] + VEC - 1, a.width);
-            rows.issue(stage, 0, v, (const T*)a.x + row * a.x_stride + at.col[v], use);
-            rows.issue(stage, 1, v, (const T*)a.dy + row * a.dy_stride + at.col[v], use);
-            if (GATE) rows.issue(stage, 2, v, (const T*)a.gate + row * a.gate_stride + at.col[v], use);
+            const bool use = at.in[v] && k < rows.mine &&
+                             SSD_INB((rows.row0 + k * s.step) * a.width + at.col[v] + VEC - 1, a.rows * a.width);
+            ring.issue(stage, 0, v, px + v * next, use);
+            ring.issue(stage, 1, v, pd + v * next, use);
+            if (GATE) ring.issue(stage, 2, v, pz + v * next, use);
         }
-        const long long m = row * a.groups + at.group;
-        const bool use = at.on && row < a.rows && SSD_INB(m, a.rows * a.groups);
-        if constexpr (rows.kRing) {
+        const bool use = k < rows.mine && SSD_INB((const float*)pst - a.stats + 1, a.rows * a.groups * 2);
+        if constexpr (Ring::kRing) {
             if (use)
-                cp_async(static_cast<uint32_t>(__cvta_generic_to_shared(moments + stage * blockDim.x)), a.stats + 2 * m,
+                cp_async(static_cast<uint32_t>(__cvta_generic_to_shared(moments + stage * blockDim.x)), pst,
                          std::integral_constant<int, 8>());
             else
                 moments[stage * blockDim.x] = make_float2(0.f, 0.f);
         } else {
-            held = use ? reinterpret_cast<const float2*>(a.stats)[m] : make_float2(0.f, 0.f);
+            held = use ? *pst : make_float2(0.f, 0.f);
         }
-        rows.commit();
+        px += s.x_step;
+        pd += s.dy_step;
+        if (GATE) pz += s.gate_step;
+        pst += s.stats_step;
+        ring.commit();
     };
     int turn = 0, stage = 0;
-    long long base = (long long)part * s.slots;
-    for (int i = 0; i < depth; ++i) fetch(base + at.slot + i * step, i);
-    for (; base < a.rows; base += step) {
-        const long long row = base + at.slot;
-        const bool live = row < a.rows && at.on;
+#pragma unroll
+    for (int i = 0; i < depth; ++i) fetch(i, i);
+    for (int k = 0; k < rows.all; ++k) {
+        const bool live = k < rows.mine;
         Pairs<VEC> xh[NV], dxh[NV];
-        rows.wait();
-        if constexpr (rows.kRing) held = moments[stage * blockDim.x];
+        ring.wait();
+        if constexpr (Ring::kRing) held = moments[stage * blockDim.x];
         const float rstd = held.y;
         float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             Pairs<VEC> x, d, z, dz;
-            rows.get(stage, 0, v, x);
-            rows.get(stage, 1, v, d);
-            if (GATE) rows.get(stage, 2, v, z);
+            ring.get(stage, 0, v, x);
+            ring.get(stage, 1, v, d);
+            if (GATE) ring.get(stage, 2, v, z);
             const float2 away = both(at.in[v] ? -held.x : 0.f);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -395,31 +445,32 @@ __global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 2 : 1)
                 s1 = add2(s1, dxh[v].p[i]);
                 s2 = tc::fma2(dxh[v].p[i], h, s2);
             }
-            if (GATE && at.in[v] && live && SSD_INB(row * a.width + at.col[v] + VEC - 1, a.rows * a.width)) {
+            if (GATE && at.in[v] && live && SSD_INB(to + v * next + VEC - 1, a.rows * a.width)) {
                 float f[VEC];
                 dz.out(f);
-                Vec<T, VEC>::store((T*)a.dgate + row * a.width + at.col[v], f);
+                Vec<T, VEC>::store((T*)a.dgate + to + v * next, f);
             }
         }
-        fetch(row + depth * step, stage);
+        fetch(k + depth, stage);
         stage = stage + 1 == depth ? 0 : stage + 1;
         float both_sums[2] = {s1.x + s1.y, s2.x + s2.y};
-        team_sum(both_sums, s.team, turn, buf);
+        team_sum(both_sums, s.team, buf[turn]);
         turn ^= 1;
         if (live) {
             const float2 m1 = both(-both_sums[0] * inv_n), m2 = both(-both_sums[1] * inv_n);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                if (!at.in[v] || !SSD_INB(row * a.width + at.col[v] + VEC - 1, a.rows * a.width)) continue;
+                if (!at.in[v] || !SSD_INB(to + v * next + VEC - 1, a.rows * a.width)) continue;
                 Pairs<VEC> dx;
 #pragma unroll
                 for (int i = 0; i < P; ++i)
                     dx.p[i] = tc::mul2(both(rstd), tc::fma2(xh[v].p[i], m2, add2(dxh[v].p[i], m1)));
                 float f[VEC];
                 dx.out(f);
-                Vec<T, VEC>::store((T*)a.dx + row * a.width + at.col[v], f);
+                Vec<T, VEC>::store((T*)a.dx + to + v * next, f);
             }
         }
+        to += s.out_step;
     }
     if (!a.part) return;
     float* pw = a.part + (size_t)part * 2 * a.width;
@@ -477,7 +528,7 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(const float* __restrict
 // Vector width, vectors per thread and the launch's shape.  A part of up to 32
 // vectors is a team of lanes; wider ones take the block, with more vectors per
 // thread only where 512 threads would not hold the part.
-int norm_shape(long long rows, int width, int groups, bool bf16, int vec, NormShape* s, int* nv) {
+int norm_shape(long long rows, int width, int groups, int vec, bool backward, NormShape* s, int* nv) {
     s->n = width / groups;
     const int v = (s->n + vec - 1) / vec;
     *nv = 1;
@@ -492,15 +543,15 @@ int norm_shape(long long rows, int width, int groups, bool bf16, int vec, NormSh
         if (s->slots > rows) s->slots = (int)rows;
         s->threads = (s->team * s->gpb * s->slots + 31) / 32 * 32;
     } else {
-        const int most = vec == 1 ? 128 : 512;
-        const int wide = vec == 1 ? 16 : 4;
-        while (*nv < wide && (v + *nv - 1) / *nv > most) *nv *= vec == 1 ? 4 : 2;
+        const int wide = vec <= 2 ? 16 : 4;
+        while (*nv < wide && (v + *nv - 1) / *nv > (vec <= 2 ? 128 : *nv == 1 ? 320 : 512)) *nv *= vec <= 2 ? 4 : 2;
         s->team = ((v + *nv - 1) / *nv + 31) / 32 * 32;
         s->gpb = s->slots = 1;
         s->threads = s->team;
     }
     s->slabs = groups / s->gpb;
-    const int per_sm = 1024 / s->threads > 0 ? 1024 / s->threads : 1;
+    const int hold = backward ? (*nv == 1 ? 640 : 512) : 1024;
+    const int per_sm = hold / s->threads > 0 ? hold / s->threads : 1;
     long long parts = (148LL * per_sm + s->slabs - 1) / s->slabs;
     const long long most = (rows + s->slots - 1) / s->slots;
     s->parts = (int)(parts < most ? parts : most);
@@ -513,7 +564,7 @@ bool aligned(const void* p, int bytes) { return ((uintptr_t)p % bytes) == 0; }
 int norm_vec(const NormArgs& a) {
     const int e = a.bf16 ? 2 : 4;
     const int n = a.width / a.groups;
-    for (int vec = 16 / e; vec >= 4; vec /= 2) {
+    for (int vec = 16 / e; vec >= 2; vec /= 2) {
         const int by = vec * e;
         if (n % vec || a.x_stride % vec || !aligned(a.x, by)) continue;
         if (a.gate && (a.gate_stride % vec || !aligned(a.gate, by))) continue;
@@ -534,6 +585,12 @@ cudaError_t launch(const NormArgs& a, NormShape s, bool backward, cudaStream_t s
                   : tensors == 2 ? Ahead<T, VEC, NV, 2>::bytes(s.threads)
                                  : Ahead<T, VEC, NV, 3>::bytes(s.threads);
     s.ring_bytes = (int)smem;
+    s.step = (long long)s.parts * s.slots;
+    s.x_step = s.step * a.x_stride;
+    s.gate_step = s.step * a.gate_stride;
+    s.dy_step = s.step * a.dy_stride;
+    s.out_step = s.step * a.width;
+    s.stats_step = s.step * a.groups;
     if (backward) {
         smem += (size_t)norm_depth(NV) * s.threads * sizeof(float2);
         const size_t sums = s.slots > 1 ? (size_t)s.slots * 2 * s.gpb * s.n * sizeof(float) : 0;
@@ -541,7 +598,7 @@ cudaError_t launch(const NormArgs& a, NormShape s, bool backward, cudaStream_t s
     }
     auto kernel = backward ? (a.gate ? layer_norm_backward_kernel<T, VEC, NV, true> : layer_norm_backward_kernel<T, VEC, NV, false>)
                            : (a.gate ? layer_norm_kernel<T, VEC, NV, true> : layer_norm_kernel<T, VEC, NV, false>);
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {  // (some KB are static)
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
@@ -552,8 +609,8 @@ cudaError_t launch(const NormArgs& a, NormShape s, bool backward, cudaStream_t s
 template <typename T, int VEC>
 cudaError_t launch_nv(const NormArgs& a, const NormShape& s, int nv, bool backward, cudaStream_t st) {
     if (nv == 1) return launch<T, VEC, 1>(a, s, backward, st);
-    if constexpr (VEC == 1) {
-        return nv == 4 ? launch<T, 1, 4>(a, s, backward, st) : launch<T, 1, 16>(a, s, backward, st);
+    if constexpr (VEC <= 2) {
+        return nv == 4 ? launch<T, VEC, 4>(a, s, backward, st) : launch<T, VEC, 16>(a, s, backward, st);
     } else {
         return nv == 2 ? launch<T, VEC, 2>(a, s, backward, st) : launch<T, VEC, 4>(a, s, backward, st);
     }
@@ -563,14 +620,17 @@ cudaError_t launch_norm(const NormArgs& a, bool backward, cudaStream_t st) {
     NormShape s;
     int nv;
     const int vec = norm_vec(a);
-    norm_shape(a.rows, a.width, a.groups, a.bf16, vec, &s, &nv);
+    norm_shape(a.rows, a.width, a.groups, vec, backward, &s, &nv);
     cudaError_t e;
     if (a.bf16)
         e = vec == 8 ? launch_nv<__nv_bfloat16, 8>(a, s, nv, backward, st)
           : vec == 4 ? launch_nv<__nv_bfloat16, 4>(a, s, nv, backward, st)
+          : vec == 2 ? launch_nv<__nv_bfloat16, 2>(a, s, nv, backward, st)
                      : launch_nv<__nv_bfloat16, 1>(a, s, nv, backward, st);
     else
-        e = vec == 4 ? launch_nv<float, 4>(a, s, nv, backward, st) : launch_nv<float, 1>(a, s, nv, backward, st);
+        e = vec == 4   ? launch_nv<float, 4>(a, s, nv, backward, st)
+            : vec == 2 ? launch_nv<float, 2>(a, s, nv, backward, st)
+                       : launch_nv<float, 1>(a, s, nv, backward, st);
     if (e != cudaSuccess || !backward || !a.part) return e;
     const dim3 grid((a.width + 31) / 32, 2);
     norm_parts_kernel<<<grid, 256, 0, st>>>(a.part, s.parts, a.width, a.dweight, a.dbias);
@@ -583,10 +643,10 @@ cudaError_t launch_layer_norm(const NormArgs& a, cudaStream_t st) { return launc
 
 int norm_backward_parts(long long rows, int width, int groups, bool bf16) {
     int most = 1;
-    for (int vec = bf16 ? 8 : 4; vec >= 1; vec = vec == 4 ? 1 : vec / 2) {
+    for (int vec = bf16 ? 8 : 4; vec >= 1; vec /= 2) {
         NormShape s;
         int nv;
-        norm_shape(rows, width, groups, bf16, vec, &s, &nv);
+        norm_shape(rows, width, groups, vec, true, &s, &nv);
         if (s.parts > most) most = s.parts;
     }
     return most;
