@@ -17,9 +17,13 @@
 //
 // The rows ahead are on their way into shared memory (cp.async, each thread the
 // elements that it will read itself, so no barrier is needed) while a row is
-// worked on: four rows of 16 bytes per thread and tensor, where one row in
-// registers left the loads' latency in the open (32768 x 5120, 80 parts, gate:
-// MEASURED_FWD).  Elements of 2 bytes, which cp.async cannot copy, are
+// worked on, where one row in registers left the loads' latency in the open
+// (32768 x 5120 in 80 groups, gate, forward: 227 us; with the ring 214).  What
+// bounds the kernels beside HBM is issuing instructions: 72 % of the issue slots
+// at 255 instructions for a vector of eight numbers, which is why arithmetic goes in
+// pairs, pointers move along, and a thread takes more than one vector.
+// Now: 32768 x 2560 forward 59.5 us (5.6 TB/s), backward 103 (4.9); 32768 x 5120 in 80
+// groups with gate 164 (6.1) and 326 (5.1).  Elements of 2 bytes, which cp.async cannot copy, are
 // prefetched one row ahead in registers.
 #include <type_traits>
 
@@ -159,7 +163,7 @@ template <> __device__ __forceinline__ float sigmoid<__nv_bfloat16>(float z) {
 
 // the most threads that norm_shape() gives a block of this variant
 constexpr int norm_threads(int vec, int nv) {
-    return (vec == 4 && nv == 4) || nv == 16 ? 1024 : nv == 1 && vec > 2 ? 320 : 512;
+    return (vec == 4 && nv == 4) || nv == 16 ? 1024 : nv == 1 ? 256 : 512;
 }
 
 // How the threads of a launch lie over rows and columns.
@@ -172,6 +176,7 @@ struct NormShape {
     int parts;   // blocks down the rows
     int threads;
     int ring_bytes;  // of the rows ahead (the backward's moments lie behind them)
+    long long most;  // blocks down the rows if each took one turn
     long long step;  // rows from one row of a thread to the next, and in numbers of each tensor
     long long x_step, gate_step, dy_step, out_step, stats_step;
 };
@@ -266,7 +271,7 @@ struct Place {
 };
 
 template <typename T, int VEC, int NV, bool GATE>
-__global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 3 : 1)
+__global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 4 : 1)
     layer_norm_kernel(const NormArgs a, const NormShape s) {
     __shared__ __align__(16) float buf[2][1][32];
     extern __shared__ __align__(16) uint8_t smem[];
@@ -525,37 +530,62 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(const float* __restrict
     }
 }
 
-// Vector width, vectors per thread and the launch's shape.  A part of up to 32
-// vectors is a team of lanes; wider ones take the block, with more vectors per
-// thread only where 512 threads would not hold the part.
-int norm_shape(long long rows, int width, int groups, int vec, bool backward, NormShape* s, int* nv) {
+// Blocks down the rows where an SM holds `resident` of them: one more than fit would
+// keep the others waiting for a second turn (32768 x 5120 in 80 groups: 166 us with
+// 296 blocks, 242 with 300).
+int norm_parts(const NormShape& s, int resident) {
+    const long long parts = 148LL * (resident > 0 ? resident : 1) / s.slabs;
+    return (int)(parts < 1 ? 1 : parts < s.most ? parts : s.most);
+}
+
+// Vectors per thread and the launch's shape.  What a row costs a thread beside its
+// numbers (sums, barriers, counting) is shared by all of them, so a thread takes two
+// vectors of a part (32768 x 2560: forward 71 us, with one 89; backward 104, with one
+// 137; 20000 x 2560 in 32 groups: 54 and 69, backward 78 and 102).  Exceptions:
+//   the gated backward of narrow parts, whose three tensors then spill registers
+//     (16384 x 1536 in 24 groups: 54 us with one, 59 with two; but 32768 x 5120
+//     in 80: 326 and 303);
+//   the plain forward of bf16 parts of more than 384 vectors takes four (16384 x 8192: 95 us,
+//     126 with two; gated 229 with four, 178 with two);
+//   what the block could not hold otherwise.
+// A part of up to 32 threads is a team of lanes, and a block takes the parts and rows
+// that leave an SM's threads busiest; wider parts take a block each.
+void norm_shape(long long rows, int width, int groups, int vec, bool gate, bool backward, NormShape* s, int* nv) {
     s->n = width / groups;
     const int v = (s->n + vec - 1) / vec;
-    *nv = 1;
-    if (v <= 32) {
+    *nv = vec > 2 && v >= 4 && (v > 32 || !(backward && gate)) ? 2 : 1;
+    // threads that an SM holds at the kernels' registers
+    const int hold = *nv == 1 && !backward ? 1024 : 512;
+    if ((v + *nv - 1) / *nv <= 32) {
         s->team = 1;
-        while (s->team < v) s->team *= 2;
-        const int teams = 256 / s->team;
-        s->gpb = 1;
-        for (int g = 1; g <= teams && g <= groups; ++g)
-            if (groups % g == 0) s->gpb = g;
-        s->slots = teams / s->gpb;
-        if (s->slots > rows) s->slots = (int)rows;
-        s->threads = (s->team * s->gpb * s->slots + 31) / 32 * 32;
+        while (s->team * *nv < v) s->team *= 2;
+        int best = 0;
+        for (int g = 1; g * s->team <= 256 && g <= groups; ++g) {
+            if (groups % g) continue;
+            for (int k = 1; k * g * s->team <= 256 && k <= rows; ++k) {
+                const int threads = (k * g * s->team + 31) / 32 * 32;
+                const int busy = hold / threads * (k * g * s->team);
+                if (busy < best) continue;
+                best = busy;
+                s->gpb = g;
+                s->slots = k;
+                s->threads = threads;
+            }
+        }
     } else {
         const int wide = vec <= 2 ? 16 : 4;
-        while (*nv < wide && (v + *nv - 1) / *nv > (vec <= 2 ? 128 : *nv == 1 ? 320 : 512)) *nv *= vec <= 2 ? 4 : 2;
+        auto most = [&] {  // threads of a block before each takes more vectors
+            if (vec <= 2) return *nv == 1 ? 128 : 512;
+            return backward || gate || vec < 8 ? 512 : 192;
+        };
+        while (*nv < wide && (v + *nv - 1) / *nv > most()) *nv *= vec <= 2 ? 4 : 2;
         s->team = ((v + *nv - 1) / *nv + 31) / 32 * 32;
         s->gpb = s->slots = 1;
         s->threads = s->team;
     }
     s->slabs = groups / s->gpb;
-    const int hold = backward ? (*nv == 1 ? 640 : 512) : 1024;
-    const int per_sm = hold / s->threads > 0 ? hold / s->threads : 1;
-    long long parts = (148LL * per_sm + s->slabs - 1) / s->slabs;
-    const long long most = (rows + s->slots - 1) / s->slots;
-    s->parts = (int)(parts < most ? parts : most);
-    return s->threads;
+    s->most = (rows + s->slots - 1) / s->slots;
+    s->parts = norm_parts(*s, (backward ? 1024 : 512) / s->threads);
 }
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p % bytes) == 0; }
@@ -577,20 +607,12 @@ int norm_vec(const NormArgs& a) {
 }
 
 template <typename T, int VEC, int NV>
-cudaError_t launch(const NormArgs& a, NormShape s, bool backward, cudaStream_t st) {
-    const long long grid = (long long)s.slabs * s.parts;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+cudaError_t launch(const NormArgs& a, NormShape& s, bool backward, cudaStream_t st) {
     const int tensors = (a.gate ? 2 : 1) + (backward ? 1 : 0);
     size_t smem = tensors == 1   ? Ahead<T, VEC, NV, 1>::bytes(s.threads)
                   : tensors == 2 ? Ahead<T, VEC, NV, 2>::bytes(s.threads)
                                  : Ahead<T, VEC, NV, 3>::bytes(s.threads);
     s.ring_bytes = (int)smem;
-    s.step = (long long)s.parts * s.slots;
-    s.x_step = s.step * a.x_stride;
-    s.gate_step = s.step * a.gate_stride;
-    s.dy_step = s.step * a.dy_stride;
-    s.out_step = s.step * a.width;
-    s.stats_step = s.step * a.groups;
     if (backward) {
         smem += (size_t)norm_depth(NV) * s.threads * sizeof(float2);
         const size_t sums = s.slots > 1 ? (size_t)s.slots * 2 * s.gpb * s.n * sizeof(float) : 0;
@@ -602,12 +624,30 @@ cudaError_t launch(const NormArgs& a, NormShape s, bool backward, cudaStream_t s
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
+    if (s.most * s.slabs > 148) {
+        int resident = 1;
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, s.threads, smem);
+        if (e != cudaSuccess) return e;
+        int parts = norm_parts(s, resident);
+        // the forward starts new blocks after some 100 rows: with 139 to a thread (32768 x
+        // 5120 in 80 groups) 164 us in two turns, 176 in one; with 74 (32768 x 2560) 62.6 and 59.5
+        if (!backward) parts = norm_parts(s, resident * (1 + (int)(s.most / parts / 96)));
+        s.parts = backward && parts > s.parts ? s.parts : parts;  // (the workspace holds that many)
+    }
+    s.step = (long long)s.parts * s.slots;
+    s.x_step = s.step * a.x_stride;
+    s.gate_step = s.step * a.gate_stride;
+    s.dy_step = s.step * a.dy_stride;
+    s.out_step = s.step * a.width;
+    s.stats_step = s.step * a.groups;
+    const long long grid = (long long)s.slabs * s.parts;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     kernel<<<(unsigned)grid, s.threads, smem, st>>>(a, s);
     return cudaGetLastError();
 }
 
 template <typename T, int VEC>
-cudaError_t launch_nv(const NormArgs& a, const NormShape& s, int nv, bool backward, cudaStream_t st) {
+cudaError_t launch_nv(const NormArgs& a, NormShape& s, int nv, bool backward, cudaStream_t st) {
     if (nv == 1) return launch<T, VEC, 1>(a, s, backward, st);
     if constexpr (VEC <= 2) {
         return nv == 4 ? launch<T, VEC, 4>(a, s, backward, st) : launch<T, VEC, 16>(a, s, backward, st);
@@ -620,7 +660,7 @@ cudaError_t launch_norm(const NormArgs& a, bool backward, cudaStream_t st) {
     NormShape s;
     int nv;
     const int vec = norm_vec(a);
-    norm_shape(a.rows, a.width, a.groups, vec, backward, &s, &nv);
+    norm_shape(a.rows, a.width, a.groups, vec, a.gate, backward, &s, &nv);
     cudaError_t e;
     if (a.bf16)
         e = vec == 8 ? launch_nv<__nv_bfloat16, 8>(a, s, nv, backward, st)
@@ -644,10 +684,12 @@ cudaError_t launch_layer_norm(const NormArgs& a, cudaStream_t st) { return launc
 int norm_backward_parts(long long rows, int width, int groups, bool bf16) {
     int most = 1;
     for (int vec = bf16 ? 8 : 4; vec >= 1; vec /= 2) {
-        NormShape s;
-        int nv;
-        norm_shape(rows, width, groups, vec, true, &s, &nv);
-        if (s.parts > most) most = s.parts;
+        for (int gate = 0; gate < 2; ++gate) {
+            NormShape s;
+            int nv;
+            norm_shape(rows, width, groups, vec, gate, true, &s, &nv);
+            if (s.parts > most) most = s.parts;
+        }
     }
     return most;
 }
