@@ -463,7 +463,11 @@ typedef struct {
  * and V multiples of 8 and rows on 16-byte boundaries (addresses, and
  * strides multiples of 8) runs on tensor cores: the masked scores and the
  * state as an operand are rounded to bf16, sums and states are fp32.
- * Everything else runs on CUDA cores in fp32.  Asynchronous on `stream`. */
+ * Everything else runs on CUDA cores in fp32.  A NaN or infinity in a token
+ * reaches that token's and later outputs of its sequence and, since the masked
+ * scores are zeros that are multiplied, earlier ones of the same 128 tokens;
+ * it never reaches another sequence.  (Padding that may hold such values goes
+ * outside the sequences, see packed.)  Asynchronous on `stream`. */
 ssd_status ssd_linear_attention(const ssd_linear_shape* shape, const void* q, const ssd_strides* q_strides,
                                 const void* k, const ssd_strides* k_strides, const void* v,
                                 const ssd_strides* v_strides, const float* decay, const int* cu_seqlens,
@@ -490,8 +494,8 @@ ssd_status ssd_linear_attention_step(const ssd_linear_shape* shape, const void* 
  *   dy [B][T][H][V] dtype, contiguous; dfinal, dinit [B][H][K][V] fp32 or NULL
  *   dq [B][T][H][K], dk [B][T][G][K], dv [B][T][G][V] dtype, contiguous; dk and
  *   dv are summed over the query heads of a group (in fp32, in a fixed order)
- * scale must not be 0.  Rows outside every packed sequence: dq is left as it
- * is; dk and dv too when H == G, undefined otherwise. */
+ * scale must not be 0.  Rows of dq, dk and dv outside every packed sequence are
+ * left as they are. */
 ssd_status ssd_linear_attention_backward(const ssd_linear_shape* shape, const void* q, const ssd_strides* q_strides,
                                          const void* k, const ssd_strides* k_strides, const void* v,
                                          const ssd_strides* v_strides, const float* decay, const int* cu_seqlens,

@@ -308,18 +308,41 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, i
     }
 }
 
-template <typename T>
+// out[row][g][d] = sum over the heads h of the group of part[row][h][d], in the order
+// of the heads, for the rows of some sequence; VEC numbers a thread, `across`
+// threads along a row (a power of two).
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256) group_sum_kernel(const float* __restrict__ part, T* __restrict__ out,
-                                                        long long total, int D, int G, int share) {
-    for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < total; e += (long long)gridDim.x * 256) {
-        const int d = (int)(e % D);
-        const long long rg = e / D;  // row * G + g
-        const float* src = part + rg * share * D + d;
-        float s = 0.f;
-        for (int h = 0; h < share; ++h)
-            if (SSD_INB(rg * share * D + d + (long long)h * D, total * share)) s += src[(long long)h * D];
-        if (SSD_INB(e, total)) out[e] = from_f32<T>(s);
+                                                        long long rows, int D, int G, int share, const int* cu,
+                                                        int B, int across) {
+    const int x = threadIdx.x % across, y = threadIdx.x / across, per = 256 / across;
+    const int units = G * D / VEC, per_group = D / VEC;
+    long long lo = 0, hi = rows;
+    if (cu) {  // (packed rows number less than 2^31)
+        lo = min(max(cu[0], 0), (int)rows);
+        hi = min(max(cu[B], 0), (int)rows);
     }
+    for (long long r = lo + (long long)blockIdx.x * per + y; r < hi; r += (long long)gridDim.x * per)
+        for (int u = x; u < units; u += across) {
+            const int g = u / per_group, d = (u - g * per_group) * VEC;
+            const long long from = ((r * G + g) * share) * D + d, to = (r * G + g) * D + d;
+            float s[VEC] = {};
+            for (int h = 0; h < share; ++h) {
+                if (!SSD_INB(from + (long long)h * D + VEC - 1, rows * G * share * D)) continue;
+                if constexpr (VEC == 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(part + from + (long long)h * D);
+                    s[0] += f.x;
+                    s[1] += f.y;
+                    s[2] += f.z;
+                    s[3] += f.w;
+                } else {
+                    s[0] += part[from + (long long)h * D];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (SSD_INB(to + i, rows * G * D)) out[to + i] = from_f32<T>(s[i]);
+        }
 }
 
 }  // namespace
@@ -357,15 +380,21 @@ cudaError_t launch_scan_combine(const ScanLaunch& s, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_group_sum(const float* part, void* out, long long rows, int H, int G, int D, bool bf16,
-                             cudaStream_t st) {
-    const long long total = rows * G * D;
-    const long long want = (total + 255) / 256;
+cudaError_t launch_group_sum(const float* part, void* out, long long rows, int H, int G, int D, const int* cu, int B,
+                             bool bf16, cudaStream_t st) {
+    const int vec = D % 4 == 0 ? 4 : 1;
+    const long long units = (long long)G * D / vec;
+    int across = 1;
+    while (across < 256 && across < units) across *= 2;
+    const long long want = (rows + 256 / across - 1) / (256 / across);
     const unsigned grid = (unsigned)(want < 148 * 16 ? want : 148 * 16);
-    if (bf16)
-        group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(part, (__nv_bfloat16*)out, total, D, G, H / G);
-    else
-        group_sum_kernel<float><<<grid, 256, 0, st>>>(part, (float*)out, total, D, G, H / G);
+    auto run = [&](auto t, auto kernel) {
+        kernel<<<grid, 256, 0, st>>>(part, (decltype(t)*)out, rows, D, G, H / G, cu, B, across);
+    };
+    if (bf16 && vec == 4) run(__nv_bfloat16(), group_sum_kernel<__nv_bfloat16, 4>);
+    else if (bf16) run(__nv_bfloat16(), group_sum_kernel<__nv_bfloat16, 1>);
+    else if (vec == 4) run(float(), group_sum_kernel<float, 4>);
+    else run(float(), group_sum_kernel<float, 1>);
     return cudaGetLastError();
 }
 

@@ -200,8 +200,8 @@ cudaError_t launch_scan_tc(const ScanLaunch& s, bool state_only, cudaStream_t st
 // states in place: slot i from "built by item i from zero" to "after item i"
 cudaError_t launch_scan_combine(const ScanLaunch& s, cudaStream_t st);
 // out[row][g][d] = sum over the heads of group g of part[row][h][d]
-cudaError_t launch_group_sum(const float* part, void* out, long long rows, int H, int G, int D, bool bf16,
-                             cudaStream_t st);
+cudaError_t launch_group_sum(const float* part, void* out, long long rows, int H, int G, int D, const int* cu, int B,
+                             bool bf16, cudaStream_t st);
 
 struct LinearStep {
     RowTensor q, k, v;

@@ -330,8 +330,10 @@ ssd_status ssd_linear_attention_backward(const ssd_linear_shape* shape, const vo
         if (e == cudaSuccess) e = run_scan(l, true, st);
     }
     if (shared) {
-        if (e == cudaSuccess) e = ssd::launch_group_sum(dk_part, dk, rows_of(s), s.H, s.G, s.K, l.bf16, st);
-        if (e == cudaSuccess) e = ssd::launch_group_sum(dv_part, dv, rows_of(s), s.H, s.G, s.V, l.bf16, st);
+        if (e == cudaSuccess) e = ssd::launch_group_sum(dk_part, dk, rows_of(s), s.H, s.G, s.K, cu_seqlens, s.B,
+                                                           l.bf16, st);
+        if (e == cudaSuccess) e = ssd::launch_group_sum(dv_part, dv, rows_of(s), s.H, s.G, s.V, cu_seqlens, s.B,
+                                                           l.bf16, st);
     }
     return status_of(e);
 }

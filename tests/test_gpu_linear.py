@@ -329,3 +329,99 @@ def test_offsets_that_are_none_stay_inside():
         y, _ = ssd.linear_attention(c["q"], c["k"], c["v"], c["decay"], cu_seqlens=cu, y=guard[128:128 + T])
         torch.cuda.synchronize()
         assert bool((guard[:128] == 3.0).all()) and bool((guard[128 + T:] == 3.0).all())
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF, 128, 64), (BF, 64, 64), (F32, 30, 24)])
+def test_packed_shared_heads(dtype, K, V):
+    """Keys and values shared by the heads of a group, rows of no sequence before
+    and behind, a workspace that held something else: the gradients of those rows are
+    zero, and nothing of the workspace reaches any."""
+    cuts, total, H, G = [5, 140, 140, 900], 960, 6, 2
+    c = make(dtype, cuts, total, H, G, K, V, outside=float("nan"))
+    both(c, cuts, dtype)
+    cu = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    code = ssd.SSD_DTYPE_BF16 if dtype == BF else ssd.SSD_DTYPE_F32
+    need = ssd.linear_backward_workspace_size(ssd.LinearShape(3, total, H, G, K, V, code, 1))
+    call = lambda fill: ssd.linear_attention_backward(  # noqa: E731
+        c["q"], c["k"], c["v"], c["decay"], c["dy"], initial_state=c["init"], dfinal=c["dfinal"], cu_seqlens=cu,
+        workspace=torch.full((need,), fill, dtype=torch.uint8, device="cuda"))
+    a, b = call(0xFF), call(0)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+        if n != "dinit":
+            assert bool((a[n][:5] == 0).all()) and bool((a[n][900:] == 0).all()) and bool(torch.isfinite(a[n]).all())
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF, 128, 64), (BF, 64, 128), (BF, 128, 128), (BF, 64, 64), (F32, 16, 16)])
+def test_many_chains(dtype, K, V):
+    """More chains than the GPU runs at a time, several chunks each, uncut in both
+    directions; gradients of all of them."""
+    B, T, H = 2, 515, 160
+    cuts = [0, T, 2 * T]
+    c = make(dtype, cuts, B * T, H, H, K, V)
+    args = (c["q"], c["k"], c["v"], c["decay"], K ** -0.5, c["init"], cuts, c["dy"], c["dfinal"])
+    ref, size = reference(*args), reference(*args, magnitude=True)
+    r = {n: c[n].view(B, T, *c[n].shape[1:]) for n in ("q", "k", "v", "dy")}
+    y, final = ssd.linear_attention(r["q"], r["k"], r["v"], c["decay"], initial_state=c["init"])
+    g = ssd.linear_attention_backward(r["q"], r["k"], r["v"], c["decay"], r["dy"], initial_state=c["init"],
+                                      dfinal=c["dfinal"])
+    got = {n: t if n in ("final", "dinit") else t.flatten(0, 1) for n, t in {"y": y, "final": final, **g}.items()}
+    check(got, ref, size, dtype, K, V, T, on_tensor_cores(dtype, K, V))
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF, 64, 64), (BF, 128, 128), (F32, 24, 16)])
+def test_many_short_sequences(dtype, K, V):
+    """Hundreds of sequences of none to nine tokens."""
+    cuts = [0]
+    for i in range(300):
+        cuts.append(cuts[-1] + (i * 7) % 10)
+    c = make(dtype, cuts, cuts[-1], 2, 1, K, V)
+    both(c, cuts, dtype)
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF, 128, 64), (BF, 64, 128), (BF, 128, 128), (BF, 64, 64), (F32, 64, 64)])
+def test_a_spoiled_sequence_stays_alone(dtype, K, V):
+    """NaN and infinities in one sequence, its ends inside the neighbours' chunks:
+    the others' results are to the bit what they are without."""
+    cuts = [0, 70, 150, 333]
+    c = make(dtype, cuts, 333, 4, 2, K, V)
+    cu = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+
+    def run():
+        y, f = ssd.linear_attention(c["q"], c["k"], c["v"], c["decay"], initial_state=c["init"], cu_seqlens=cu)
+        g = ssd.linear_attention_backward(c["q"], c["k"], c["v"], c["decay"], c["dy"], initial_state=c["init"],
+                                          dfinal=c["dfinal"], cu_seqlens=cu)
+        return {"y": y, "final": f, **g}
+
+    want = run()
+    for n in ("q", "k", "v", "dy"):
+        c[n][70:110] = float("nan")
+        c[n][110:150] = float("inf")
+    got = run()
+    for n, t in got.items():
+        for keep in ([slice(0, 1), slice(2, 3)] if n in ("final", "dinit") else [slice(0, 70), slice(150, 333)]):
+            assert torch.equal(t[keep], want[n][keep]), n
+
+
+def test_refusals_on_the_gpu():
+    """Wrong types, shapes, devices and layouts are errors of the call."""
+    c = make(BF, [0, 40], 40, 4, 2, 64, 64)
+    q, k, v, decay = c["q"][None], c["k"][None], c["v"][None], c["decay"]
+    ok = ssd.linear_attention(q, k, v, decay)[0]
+    for bad in [dict(q=q.half()), dict(k=k.float()), dict(v=v[:, :30]), dict(k=k[:, :, :1].expand(1, 40, 3, 64)),
+                dict(decay=decay.double()), dict(decay=decay[:3]), dict(decay=decay.cpu()), dict(q=q[..., :40]),
+                dict(q=q.transpose(2, 3).contiguous().transpose(2, 3)), dict(initial_state=c["init"].half()),
+                dict(initial_state=c["init"][:, :2]), dict(y=torch.empty_like(ok).transpose(1, 2)),
+                dict(y=ok.float()), dict(workspace=torch.empty(1, dtype=torch.uint8, device="cuda")),
+                dict(cu_seqlens=torch.zeros(2, dtype=torch.int32, device="cuda")),
+                dict(scale=float("nan")), dict(q=q[:, :0], k=k[:, :0], v=v[:, :0])]:
+        with pytest.raises((ValueError, ssd.SSDError)):
+            ssd.linear_attention(**{**dict(q=q, k=k, v=v, decay=decay), **bad})
+    with pytest.raises((ValueError, ssd.SSDError)):
+        ssd.linear_attention_backward(q, k, v, decay, c["dy"][None], scale=0.0)
+    with pytest.raises((ValueError, ssd.SSDError)):
+        ssd.linear_attention_backward(q, k, v, decay, c["dy"][None].float())
+    with pytest.raises((ValueError, ssd.SSDError)):
+        ssd.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], decay, c["init"].transpose(2, 3))
+    torch.cuda.synchronize()
+    assert torch.equal(ssd.linear_attention(q, k, v, decay)[0], ok)
