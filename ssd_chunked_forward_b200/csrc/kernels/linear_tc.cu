@@ -81,7 +81,7 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t adv_bytes) {
 }
 
 struct TcParams {
-    CUtensorMap map[kScanRoles][4];  // q, k, v, out
+    CUtensorMap map[kScanRoles][4];
     ScanLaunch s;
 };
 
@@ -215,7 +215,18 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     const int span = it.t1 - it.t0;
     const int nch = (span + kBlk - 1) / kBlk;
 
-    if (threadIdx.x == 32) {
+    // first token (in the sequence) and tokens of the c-th chunk in scan order
+    auto chunk_at = [&](int c) -> int { return it.t0 + (rev ? nch - 1 - c : c) * kBlk; };
+    auto chunk_n = [&](int t) -> int { return min(kBlk, it.t1 - t); };
+    auto load_tile = [&](int c, int w, int head) {
+        const auto b = L::buf(c, w);
+        const int panels = (w == 2 ? VP : KP) / 64;
+        tc::mbar_arrive_expect_tx(&bars->full[b.i], panels * kPanel);
+        for (int x = 0; x < panels; ++x)
+            tc::tma_load_4d(sm + b.off + x * kPanel, &p.map[it.role][w], &bars->full[b.i], 64 * x, head,
+                            (int)(it.row0 + chunk_at(c)), it.batch);
+    };
+    if (warp == kLoads && lane == 0) {
         for (int i = 0; i < L::kBufs; ++i) {
             // a tile's place is free again when both its products are done (q: S, Q H;
             // k: S, Z; v: P V, Z) and, in the ring, v's output has left
@@ -246,7 +257,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         tc::mbar_init(&bars->s_done, 1);
         tc::mbar_init(&bars->done, 1);
         tc::fence_mbar_init();
+        tc::fence_proxy_async_smem();
+        // the first chunk's tiles, while the others make the tables
+        if (nch > 0)
+            for (int w = kOut ? 0 : 1; w < 3; ++w)
+                load_tile(0, w, it.head / (w == 0 ? R.q.share : w == 1 ? R.k.share : R.v.share));
     }
+    __syncwarp();
     if (warp == kOutputs) {
         tc::tmem_alloc(sTmem, 512);
         tc::tmem_relinquish();
@@ -288,9 +305,6 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         tc::mma_commit_if(e, &bars->empty[buf]);
         if (kOut && L::kRing && in_ring == 2) tc::mma_commit_if(e, &bars->empty[buf]);
     };
-    // first token (in the sequence) and tokens of the c-th chunk in scan order
-    auto chunk_at = [&](int c) -> int { return it.t0 + (rev ? nch - 1 - c : c) * kBlk; };
-    auto chunk_n = [&](int t) -> int { return min(kBlk, it.t1 - t); };
     // a chunk of n tokens whose output leaves by plain stores: fp32, or a packed
     // sequence's end, behind which the rows are another's
     auto direct = [&](int n) -> bool { return out_f32 || (packed && n < kBlk); };
@@ -300,21 +314,15 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             // ------------------------------------------------- TMA loads ----
             // (unrolled: with rolled loops the loads went out later, 40 us of 450)
             bool ok = true;
-            const int hq = it.head / R.q.share;
-            const int hk = it.head / R.k.share, hv = it.head / R.v.share;
-            int c = 0;
+            const int hq = it.head / R.q.share, hk = it.head / R.k.share, hv = it.head / R.v.share;
+            int c = 1;
 #pragma unroll 1
             for (; ok && c < nch; ++c) {
-                const int row = (int)(it.row0 + chunk_at(c));
 #pragma unroll
                 for (int w = kOut ? 0 : 1; w < 3; ++w) {
                     const auto b = L::buf(c, w);
                     if (b.use > 0 && !wait(&bars->empty[b.i], (b.use - 1) & 1)) { ok = false; break; }
-                    const int panels = (w == 2 ? VP : KP) / 64;
-                    tc::mbar_arrive_expect_tx(&bars->full[b.i], panels * kPanel);
-                    for (int x = 0; x < panels; ++x)
-                        tc::tma_load_4d(sm + b.off + x * kPanel, &p.map[it.role][w], &bars->full[b.i], 64 * x,
-                                        w == 0 ? hq : w == 1 ? hk : hv, row, it.batch);
+                    load_tile(c, w, w == 0 ? hq : w == 1 ? hk : hv);
                 }
             }
             if (!ok) {
@@ -481,13 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 ok = wait_warp(&bars->full[bk.i], bk.use & 1) && wait_warp(&bars->full[bv.i], bv.use & 1) &&
                      (!kOut || wait_warp(&bars->s_full[c & 1], (c >> 1) & 1));
                 if (!ok) break;
-                const int each = (kBlk - n) * 8;
-                for (int e = threadIdx.x; e < each * (KP / 64 + VP / 64); e += 256) {
-                    const int x = e / each, f = e - x * each;
-                    const uint32_t off = x < KP / 64 ? bk.off + x * kPanel : bv.off + (x - KP / 64) * kPanel;
-                    // where pieces go in place, the rows belong to their part's warps
-                    if (!(L::kInPlace && x < KP / 64))
-                        *reinterpret_cast<uint4*>(sm + off + (n + f / 8) * 128 + (f & 7) * 16) = make_uint4(0, 0, 0, 0);
+                // a row's panels of k, then of v: eight lanes each; where pieces go in place,
+                // k's rows belong to their part's warps
+                const int x = lane >> 3;
+                if (x < (KP + VP) / 64 && !(L::kInPlace && x < KP / 64)) {
+                    uint8_t* at = sm + (x < KP / 64 ? bk.off + x * kPanel : bv.off + (x - KP / 64) * kPanel) + (lane & 7) * 16;
+                    for (int f = n + warp; f < kBlk; f += 8)
+                        *reinterpret_cast<uint4*>(at + f * 128) = make_uint4(0, 0, 0, 0);
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
@@ -613,10 +621,22 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             src += k_of(0) * sk + v_of(0) * sv;
             const long long step = kLaneV ? sk : sv;
             const int have = kLaneV ? (lr < V ? K - c0 : 0) : (lr < K ? V - c0 : 0);
+            if (step == 1) {  // the thread's columns are neighbours (K and V are multiples of 8)
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                if (c < have && SSD_INB(k_of(c) * sk + v_of(c) * sv, (long long)K * V)) h[c] = *src * mul;
-                src += step;
+                for (int c = 0; c < CH; c += 4)
+                    if (c < have && SSD_INB(k_of(c) * sk + v_of(c) * sv + 3, (long long)K * V)) {
+                        const float4 f = *reinterpret_cast<const float4*>(src + c);
+                        h[c] = f.x * mul;
+                        h[c + 1] = f.y * mul;
+                        h[c + 2] = f.z * mul;
+                        h[c + 3] = f.w * mul;
+                    }
+            } else {  // the lanes' are
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    if (c < have && SSD_INB(k_of(c) * sk + v_of(c) * sv, (long long)K * V)) h[c] = *src * mul;
+                    src += step;
+                }
             }
         }
         // H as an operand: [v][k] (lanes v) or [k][v]
@@ -749,12 +769,19 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         }
         if (ok && dst && holds && SSD_INB(kOut ? chain : it.slot, kOut ? chains : p.s.plan.slots())) {
             dst += (long long)k_of(0) * V + v_of(0);
-            const int step = kLaneV ? V : 1;
             const int have = kLaneV ? (lr < V ? K - c0 : 0) : (lr < K ? V - c0 : 0);
+            if constexpr (kLaneV) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                if (c < have) *dst = h[c] * mul;
-                dst += step;
+                for (int c = 0; c < CH; ++c) {
+                    if (c < have) *dst = h[c] * mul;
+                    dst += V;
+                }
+            } else {  // (32 single stores of rows by their threads: 8000 cycles)
+#pragma unroll
+                for (int c = 0; c < CH; c += 4)
+                    if (c < have)
+                        *reinterpret_cast<float4*>(dst + c) =
+                            make_float4(h[c] * mul, h[c + 1] * mul, h[c + 2] * mul, h[c + 3] * mul);
             }
         }
     }
@@ -801,20 +828,21 @@ cudaError_t launch_dims(const TcParams& p, bool state_only, cudaStream_t st) {
 
 }  // namespace
 
-bool scan_tc_supported(const ScanRole& r, const ScanPlan& p, bool bf16) {
-    if (!bf16 || r.K > 128 || r.V > 128 || r.K % 8 != 0 || r.V % 8 != 0) return false;
-    CUtensorMap m[4];
-    return role_maps(r, p, m) == cudaSuccess;
+bool scan_tc_maps(const ScanLaunch& s, ScanMaps& m) {
+    static_assert(sizeof(m.map) == sizeof(CUtensorMap) * kScanRoles * 4, "tensor maps");
+    for (int i = 0; i < s.plan.nroles; ++i) {
+        const ScanRole& r = s.role[i];
+        if (!s.bf16 || r.K > 128 || r.V > 128 || r.K % 8 != 0 || r.V % 8 != 0) return false;
+        if (role_maps(r, s.plan, reinterpret_cast<CUtensorMap*>(m.map[i])) != cudaSuccess) return false;
+    }
+    return true;
 }
 
-cudaError_t launch_scan_tc(const ScanLaunch& s, bool state_only, cudaStream_t st) {
+cudaError_t launch_scan_tc(const ScanLaunch& s, const ScanMaps& m, bool state_only, cudaStream_t st) {
     if (s.plan.items > 0x7fffffffLL) return cudaErrorInvalidValue;
     TcParams p;
     p.s = s;
-    for (int r = 0; r < kScanRoles; ++r) {
-        cudaError_t e = role_maps(s.role[r < s.plan.nroles ? r : 0], s.plan, p.map[r]);
-        if (e != cudaSuccess) return e;
-    }
+    memcpy(p.map, m.map, sizeof(CUtensorMap) * 4 * s.plan.nroles);
     const int k = padded(s.role[0].K), v = padded(s.role[0].V);
     if (k == 64) return v == 64 ? launch_dims<64, 64>(p, state_only, st) : launch_dims<64, 128>(p, state_only, st);
     return v == 64 ? launch_dims<128, 64>(p, state_only, st) : launch_dims<128, 128>(p, state_only, st);

@@ -99,22 +99,24 @@ __device__ inline ScanItem scan_item(const ScanPlan& p, long long it) {
     ScanItem r;
     r.valid = 0;
     r.row0 = 0;
+    // an item is a block of a grid: 32 bits hold it, and their divisions are short.
+    // (Packed offsets that decrease can ask for more items than there are slots for.)
+    if (it >= p.items) return r;
     if (!p.packed) {
-        long long cr = it;
+        unsigned cr = (unsigned)it;
         int seg = 0, nseg = 1;
         r.slot = -1;
         if (it >= p.nfull) {
-            const long long rest = it - p.nfull;
-            cr = p.nfull + rest / p.nseg;
-            seg = (int)(rest % p.nseg);
+            const unsigned rest = cr - (unsigned)p.nfull, chain = rest / (unsigned)p.nseg;
+            cr = (unsigned)p.nfull + chain;
+            seg = (int)(rest - chain * (unsigned)p.nseg);
             nseg = p.nseg;
             r.slot = rest;
         }
-        if (it >= p.items) return r;
-        r.role = (int)(cr % p.nroles);
-        cr /= p.nroles;
-        r.head = (int)(cr % p.H);
-        r.seq = (int)(cr / p.H);
+        const unsigned hr = p.nroles == 1 ? cr : cr / (unsigned)p.nroles;
+        r.role = (int)(cr - hr * (unsigned)p.nroles);
+        r.seq = (int)(hr / (unsigned)p.H);
+        r.head = (int)(hr - (unsigned)r.seq * (unsigned)p.H);
         r.batch = r.seq;
         r.len = p.T;
         r.seg = seg;
@@ -124,10 +126,10 @@ __device__ inline ScanItem scan_item(const ScanPlan& p, long long it) {
     } else {
         const int lane = threadIdx.x & 31;
         const int HR = p.H * p.nroles;
-        const long long unit = it / HR;
-        const int hr = (int)(it % HR);
-        r.role = hr % p.nroles;
+        const long long unit = (unsigned)it / (unsigned)HR;
+        const int hr = (int)((unsigned)it - (unsigned)unit * (unsigned)HR);
         r.head = hr / p.nroles;
+        r.role = hr - r.head * p.nroles;
         r.batch = 0;
         long long before = 0;
         int found = 0;
@@ -158,8 +160,7 @@ __device__ inline ScanItem scan_item(const ScanPlan& p, long long it) {
                 before += __shfl_sync(0xffffffffu, sum, 31);
             }
         }
-        // offsets that decrease can ask for more items than there are slots for
-        if (!found || it >= p.items) return r;
+        if (!found) return r;
         r.slot = it;
         r.slot_prev = r.seg > 0 ? it - HR : -1;
         r.valid = 1;
@@ -195,8 +196,10 @@ static __device__ __noinline__ float2 decay_power(float decay, int n) {
 cudaError_t launch_scan_simt(const ScanLaunch& s, bool state_only, cudaStream_t st);
 // Tensor cores (linear_tc.cu): bf16, sizes up to 128 and multiples of 8, rows
 // on 16-byte boundaries.
-bool scan_tc_supported(const ScanRole& r, const ScanPlan& p, bool bf16);
-cudaError_t launch_scan_tc(const ScanLaunch& s, bool state_only, cudaStream_t st);
+struct ScanMaps { alignas(64) unsigned char map[kScanRoles][4][128]; };  // CUtensorMap of q, k, v and out
+// the roles' maps; false: not for this kernel
+bool scan_tc_maps(const ScanLaunch& s, ScanMaps& m);
+cudaError_t launch_scan_tc(const ScanLaunch& s, const ScanMaps& m, bool state_only, cudaStream_t st);
 // states in place: slot i from "built by item i from zero" to "after item i"
 cudaError_t launch_scan_combine(const ScanLaunch& s, cudaStream_t st);
 // out[row][g][d] = sum over the heads of group g of part[row][h][d]

@@ -153,22 +153,17 @@ size_t slots_bytes(const ssd_linear_shape& s, int nroles, int vmax, bool backwar
 long long rows_of(const ssd_linear_shape& s) { return s.packed ? s.T : (long long)s.B * s.T; }
 
 // One scan launch: states of the cut chains, their combination, the outputs.
-cudaError_t run_scan(ScanLaunch& l, bool tc, cudaStream_t st) {
+// maps: for the tensor cores, null = CUDA cores
+cudaError_t run_scan(ScanLaunch& l, const ssd::ScanMaps* maps, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     if (l.plan.cut()) {
-        e = tc ? ssd::launch_scan_tc(l, true, st) : ssd::launch_scan_simt(l, true, st);
+        e = maps ? ssd::launch_scan_tc(l, *maps, true, st) : ssd::launch_scan_simt(l, true, st);
         l.reset = 0;
         if (e == cudaSuccess) e = ssd::launch_scan_combine(l, st);
     }
-    if (e == cudaSuccess) e = tc ? ssd::launch_scan_tc(l, false, st) : ssd::launch_scan_simt(l, false, st);
+    if (e == cudaSuccess) e = maps ? ssd::launch_scan_tc(l, *maps, false, st) : ssd::launch_scan_simt(l, false, st);
     l.reset = 0;
     return e;
-}
-
-bool tc_serves(const ScanLaunch& l) {
-    for (int r = 0; r < l.plan.nroles; ++r)
-        if (!ssd::scan_tc_supported(l.role[r], l.plan, l.bf16)) return false;
-    return true;
 }
 
 }  // namespace
@@ -215,9 +210,10 @@ ssd_status ssd_linear_attention(const ssd_linear_shape* shape, const void* q, co
     r.fin = final_state;
     r.fin_scale = 1.f;
     l.plan = make_plan(s, 1, s.V, true, cu_seqlens);
-    const bool tc = tc_serves(l);
+    ssd::ScanMaps maps;
+    const bool tc = ssd::scan_tc_maps(l, maps);
     if (!tc) l.plan = make_plan(s, 1, s.V, false, cu_seqlens);
-    return status_of(run_scan(l, tc, (cudaStream_t)stream));
+    return status_of(run_scan(l, tc ? &maps : nullptr, (cudaStream_t)stream));
 }
 
 ssd_status ssd_linear_attention_step(const ssd_linear_shape* shape, const void* q, const ssd_strides* q_strides,
@@ -317,17 +313,19 @@ ssd_status ssd_linear_attention_backward(const ssd_linear_shape* shape, const vo
     l.role[2] = c;
     l.plan = make_plan(s, 3, vmax, true, cu_seqlens);
     cudaError_t e;
-    if (!tc_serves(l)) {
+    ssd::ScanMaps maps;
+    if (!ssd::scan_tc_maps(l, maps)) {
         l.plan = make_plan(s, 3, vmax, false, cu_seqlens);
-        e = run_scan(l, false, st);
+        e = run_scan(l, nullptr, st);
     } else if (pad64(s.K) == pad64(s.V)) {
-        e = run_scan(l, true, st);
+        e = run_scan(l, &maps, st);
     } else {  // dq and dk have the state [V][K], dv has [K][V]: other tiles
         l.plan = make_plan(s, 2, vmax, true, cu_seqlens);
-        e = run_scan(l, true, st);
+        e = run_scan(l, &maps, st);
         l.role[0] = c;
+        memcpy(maps.map[0], maps.map[2], sizeof maps.map[0]);
         l.plan = make_plan(s, 1, vmax, true, cu_seqlens);
-        if (e == cudaSuccess) e = run_scan(l, true, st);
+        if (e == cudaSuccess) e = run_scan(l, &maps, st);
     }
     if (shared) {
         if (e == cudaSuccess) e = ssd::launch_group_sum(dk_part, dk, rows_of(s), s.H, s.G, s.K, cu_seqlens, s.B,
