@@ -363,6 +363,7 @@ template <typename T, int VEC, int NV, bool GATE>
 __global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 2 : 1)
     layer_norm_backward_kernel(const NormArgs a, const NormShape s) {
     extern __shared__ __align__(16) uint8_t smem[];
+    next_may_start();
     float* sums = reinterpret_cast<float*>(smem);  // at the end: [slots][2][cols of the block], when slots > 1
     __shared__ __align__(16) float buf[2][2][32];
     constexpr int P = Pairs<VEC>::N, NT = GATE ? 3 : 2;
@@ -511,16 +512,17 @@ __global__ void __launch_bounds__(norm_threads(VEC, NV), NV == 1 ? 2 : 1)
 
 // dweight and dbias: column c of part[p][0 or 1], added over p.  32 columns of
 // one of the two by 8 slices of the rows per block.
-__global__ void __launch_bounds__(256) norm_parts_kernel(const float* __restrict__ part, int parts, int width,
-                                                         float* __restrict__ dweight, float* __restrict__ dbias) {
+__global__ void __launch_bounds__(256) norm_parts_kernel(const float* part, int parts, int width, float* dweight,
+                                                         float* dbias) {
     __shared__ float s[8][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + x, which = blockIdx.y;
+    const int c = (blockIdx.x >> 1) * 32 + x, which = blockIdx.x & 1;
+    wait_for_earlier();
     float t = 0.f;
     if (c < width)
         for (int p = y; p < parts; p += 8)
             if (SSD_INB(((long long)p * 2 + which) * width + c, (long long)parts * 2 * width))
-                t += part[((size_t)p * 2 + which) * width + c];
+                t += __ldcg(part + ((size_t)p * 2 + which) * width + c);
     s[y][x] = t;
     __syncthreads();
     if (y == 0 && c < width) {
@@ -672,9 +674,8 @@ cudaError_t launch_norm(const NormArgs& a, bool backward, cudaStream_t st) {
             : vec == 2 ? launch_nv<float, 2>(a, s, nv, backward, st)
                        : launch_nv<float, 1>(a, s, nv, backward, st);
     if (e != cudaSuccess || !backward || !a.part) return e;
-    const dim3 grid((a.width + 31) / 32, 2);
-    norm_parts_kernel<<<grid, 256, 0, st>>>(a.part, s.parts, a.width, a.dweight, a.dbias);
-    return cudaGetLastError();
+    return launch_in_call(norm_parts_kernel, (unsigned)((a.width + 31) / 32 * 2), 256, 0, st, true,
+                          (const float*)a.part, s.parts, a.width, a.dweight, a.dbias);
 }
 
 }  // namespace

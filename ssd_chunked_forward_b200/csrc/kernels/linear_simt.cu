@@ -53,6 +53,7 @@ template <typename T, bool kOut>
 __global__ void __launch_bounds__(kThreads) scan_simt_kernel(const ScanLaunch p, int ntiles) {
     extern __shared__ __align__(16) float sm[];
     __shared__ ScanItem sItem;
+    next_may_start();
     if (p.reset && blockIdx.x == 0 && threadIdx.x == 0) *p.status = kDevOk;
     if (threadIdx.x < 32) {
         ScanItem it = scan_item(p.plan, blockIdx.x / ntiles);
@@ -60,6 +61,7 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(const ScanLaunch p,
         if (threadIdx.x == 0) sItem = it;
     }
     __syncthreads();
+    wait_for_earlier();
     const ScanItem it = sItem;
     if (!it.valid || (!kOut && it.seg == it.nseg - 1)) return;
     const ScanRole& R = p.role[it.role];
@@ -247,6 +249,7 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(const ScanLaunch p,
 // per state element at a time; the work is one pass over the slots.
 __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, int tiles) {
     __shared__ ScanItem sItem;
+    next_may_start();
     const int HR = p.plan.H * p.plan.nroles;
     const long long cr = blockIdx.x / tiles;  // chain and role
     if (threadIdx.x < 32) {
@@ -279,7 +282,10 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, i
     }
     __syncthreads();
     const ScanItem it = sItem;
-    if (!it.valid || it.nseg < 2) return;
+    if (!it.valid || it.nseg < 2) {
+        if (blockIdx.x == 0) wait_for_earlier();
+        return;
+    }
     const ScanRole& R = p.role[it.role];
     const int K = R.K, V = R.V;
     const float la = p.decay[it.head];
@@ -290,6 +296,7 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, i
     // and its initial state meets the last token undecayed
     const int n0 = R.reverse ? it.len - (it.nseg - 1) * p.plan.seg_tokens - 1 : p.plan.seg_tokens;
     const float2 first = decay_power(la, n0);
+    wait_for_earlier();
     for (int e = (blockIdx.x % tiles) * 256 + threadIdx.x; e < K * V; e += tiles * 256) {
         float h = 0.f;
         if (R.init) {
@@ -312,9 +319,10 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, i
 // of the heads, for the rows of some sequence; VEC numbers a thread, `across`
 // threads along a row (a power of two).
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) group_sum_kernel(const float* __restrict__ part, T* __restrict__ out,
-                                                        long long rows, int D, int G, int share, const int* cu,
-                                                        int B, int across) {
+__global__ void __launch_bounds__(256) group_sum_kernel(const float* part, T* out, long long rows, int D,
+                                                        int G, int share, const int* cu, int B, int across) {
+    next_may_start();
+    wait_for_earlier();
     const int x = threadIdx.x % across, y = threadIdx.x / across, per = 256 / across;
     const int units = G * D / VEC, per_group = D / VEC;
     long long lo = 0, hi = rows;
@@ -330,13 +338,13 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float* __restrict_
             for (int h = 0; h < share; ++h) {
                 if (!SSD_INB(from + (long long)h * D + VEC - 1, rows * G * share * D)) continue;
                 if constexpr (VEC == 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(part + from + (long long)h * D);
+                    const float4 f = __ldcg(reinterpret_cast<const float4*>(part + from + (long long)h * D));
                     s[0] += f.x;
                     s[1] += f.y;
                     s[2] += f.z;
                     s[3] += f.w;
                 } else {
-                    s[0] += part[from + (long long)h * D];
+                    s[0] += __ldcg(part + from + (long long)h * D);
                 }
             }
 #pragma unroll
@@ -361,8 +369,7 @@ cudaError_t launch_scan_simt(const ScanLaunch& s, bool state_only, cudaStream_t 
                          : (state_only ? scan_simt_kernel<float, false> : scan_simt_kernel<float, true>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)grid, kThreads, smem, st>>>(s, ntiles);
-    return cudaGetLastError();
+    return launch_in_call(kernel, (unsigned)grid, kThreads, smem, st, !s.reset, s, ntiles);
 }
 
 cudaError_t launch_scan_combine(const ScanLaunch& s, cudaStream_t st) {
@@ -376,8 +383,7 @@ cudaError_t launch_scan_combine(const ScanLaunch& s, cudaStream_t st) {
     while (tiles > 1 && chains * tiles > 148 * 16) tiles = (tiles + 1) / 2;
     const long long grid = chains * tiles;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    scan_combine_kernel<<<(unsigned)grid, 256, 0, st>>>(s, tiles);
-    return cudaGetLastError();
+    return launch_in_call(scan_combine_kernel, (unsigned)grid, 256, 0, st, true, s, tiles);
 }
 
 cudaError_t launch_group_sum(const float* part, void* out, long long rows, int H, int G, int D, const int* cu, int B,
@@ -388,14 +394,13 @@ cudaError_t launch_group_sum(const float* part, void* out, long long rows, int H
     while (across < 256 && across < units) across *= 2;
     const long long want = (rows + 256 / across - 1) / (256 / across);
     const unsigned grid = (unsigned)(want < 148 * 16 ? want : 148 * 16);
-    auto run = [&](auto t, auto kernel) {
-        kernel<<<grid, 256, 0, st>>>(part, (decltype(t)*)out, rows, D, G, H / G, cu, B, across);
+    auto run = [&](auto kernel, auto to) {
+        return launch_in_call(kernel, grid, 256, 0, st, true, part, to, rows, D, G, H / G, cu, B, across);
     };
-    if (bf16 && vec == 4) run(__nv_bfloat16(), group_sum_kernel<__nv_bfloat16, 4>);
-    else if (bf16) run(__nv_bfloat16(), group_sum_kernel<__nv_bfloat16, 1>);
-    else if (vec == 4) run(float(), group_sum_kernel<float, 4>);
-    else run(float(), group_sum_kernel<float, 1>);
-    return cudaGetLastError();
+    auto* b = (__nv_bfloat16*)out;
+    auto* f = (float*)out;
+    if (bf16) return vec == 4 ? run(group_sum_kernel<__nv_bfloat16, 4>, b) : run(group_sum_kernel<__nv_bfloat16, 1>, b);
+    return vec == 4 ? run(group_sum_kernel<float, 4>, f) : run(group_sum_kernel<float, 1>, f);
 }
 
 }  // namespace ssd

@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     ScanItem* sItem = reinterpret_cast<ScanItem*>(sm + L::OFF_ITEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    next_may_start();
     if (p.s.reset && blockIdx.x == 0 && threadIdx.x == 0) *p.s.status = kDevOk;
     if (warp == 0) {
         ScanItem f = scan_item(p.s.plan, blockIdx.x);
@@ -201,7 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     }
     __syncthreads();
     const ScanItem it = *sItem;
-    if (!it.valid || (!kOut && it.seg == it.nseg - 1)) return;
+    if (!it.valid || (!kOut && it.seg == it.nseg - 1)) {
+        if (blockIdx.x == 0) wait_for_earlier();
+        return;
+    }
     const ScanRole& R = p.s.role[it.role];
     const int K = R.K, V = R.V;
     const bool rev = R.reverse != 0;
@@ -614,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         auto v_of = [&](int c) -> int { return kLaneV ? lr : c0 + c; };
 #pragma unroll
         for (int c = 0; c < CH; ++c) h[c] = 0.f;
+        if (kOut && !from_init) wait_for_earlier();
         if (kOut && holds && (!from_init || R.init)) {
             const float* src = from_init ? R.init + chain * K * V : p.s.states + it.slot_prev * K * V;
             const long long sk = from_init ? R.init_k : V, sv = from_init ? R.init_v : 1;
@@ -759,6 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         }
         if (!ok) fail();
         // the state after the item
+        wait_for_earlier();
         float* dst = nullptr;
         float mul = 1.f;
         if (!kOut) {
@@ -814,8 +820,7 @@ cudaError_t launch(const TcParams& p, cudaStream_t st) {
     constexpr size_t smem = Layout<KP, VP, kOut, kPieces>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)p.s.plan.items, kThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_in_call(kernel, (unsigned)p.s.plan.items, kThreads, smem, st, !p.s.reset, p);
 }
 
 template <int KP, int VP>

@@ -190,6 +190,34 @@ static __device__ __noinline__ float2 decay_power(float decay, int n) {
 }
 #endif
 
+#ifdef __CUDACC__
+// Kernels of one call overlap at their ends: a kernel lets the next one's blocks start
+// as soon as all of its own have (they take the places that its last ones leave, and
+// make their tables), and a block waits, before it touches what an earlier kernel
+// reads or writes, until all kernels before its own are done.  Some block of each
+// kernel waits in any case, so that a kernel is never done before the earlier ones.
+// (Gradients of 32768 x 2560 norms 104 -> 97 us, 24 packed prompts 172 -> 166.)
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// kernel<<<grid, block, smem, st>>>(args); behind: it follows a kernel of the same call
+template <typename... P, typename... A>
+cudaError_t launch_in_call(void (*kernel)(P...), unsigned grid, int block, size_t smem, cudaStream_t st, bool behind,
+                           const A&... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3((unsigned)block);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = at;
+    c.numAttrs = behind ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
+#endif
+
 // ---- launchers --------------------------------------------------------------
 // CUDA cores, fp32 arithmetic: any sizes up to 256, any strides.  state_only:
 // the states of the items that are not their chain's last, into `states`.
