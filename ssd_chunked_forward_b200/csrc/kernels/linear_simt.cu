@@ -297,20 +297,36 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, i
     const int n0 = R.reverse ? it.len - (it.nseg - 1) * p.plan.seg_tokens - 1 : p.plan.seg_tokens;
     const float2 first = decay_power(la, n0);
     wait_for_earlier();
-    for (int e = (blockIdx.x % tiles) * 256 + threadIdx.x; e < K * V; e += tiles * 256) {
-        float h = 0.f;
-        if (R.init) {
-            const long long at = chain * K * V + (e / V) * R.init_k + (e % V) * R.init_v;
-            if (SSD_INB(at, (long long)p.plan.B * p.plan.H * K * V)) h = R.init[at] * R.init_scale;
+    // four elements at a time: their loads are on the way together
+    constexpr int U = 4;
+    const int apart = tiles * 256, KV = K * V;
+    for (int e0 = (blockIdx.x % tiles) * 256 + threadIdx.x; e0 < KV; e0 += U * apart) {
+        float h[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = e0 + u * apart;
+            h[u] = 0.f;
+            if (R.init && e < KV) {
+                const long long at = chain * KV + (e / V) * R.init_k + (e % V) * R.init_v;
+                if (SSD_INB(at, (long long)p.plan.B * p.plan.H * KV)) h[u] = R.init[at] * R.init_scale;
+            }
         }
         for (int i = 0; i + 1 < it.nseg; ++i) {
             const long long slot = it.slot + i * step;
             if (slot >= p.plan.slots()) break;  // decreasing offsets: the items behind do not run
-            const long long at = slot * K * V + e;
-            if (!SSD_INB(at, p.plan.slots() * K * V)) break;
             const float2 d = i == 0 ? first : whole;
-            h = fmaf(h, d.x, fmaf(h, d.y, p.states[at]));
-            p.states[at] = h;
+            float z[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const long long at = slot * KV + e0 + u * apart;
+                z[u] = e0 + u * apart < KV && SSD_INB(at, p.plan.slots() * KV) ? p.states[at] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const long long at = slot * KV + e0 + u * apart;
+                h[u] = fmaf(h[u], d.x, fmaf(h[u], d.y, z[u]));
+                if (e0 + u * apart < KV && SSD_INB(at, p.plan.slots() * KV)) p.states[at] = h[u];
+            }
         }
     }
 }
@@ -379,8 +395,8 @@ cudaError_t launch_scan_combine(const ScanLaunch& s, cudaStream_t st) {
     // blocks find an uncut chain and leave
     const long long all = (long long)s.plan.B * s.plan.H * s.plan.nroles;
     const long long chains = s.plan.packed ? all : all - s.plan.nfull;
-    int tiles = (KV + 255) / 256;
-    while (tiles > 1 && chains * tiles > 148 * 16) tiles = (tiles + 1) / 2;
+    int tiles = (KV + 1023) / 1024;  // (four elements a thread)
+    while (tiles > 1 && chains * tiles > 148 * 8) tiles = (tiles + 1) / 2;
     const long long grid = chains * tiles;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_in_call(scan_combine_kernel, (unsigned)grid, 256, 0, st, true, s, tiles);
