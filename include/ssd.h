@@ -464,10 +464,8 @@ typedef struct {
  * strides multiples of 8) runs on tensor cores: the masked scores and the
  * state as an operand are rounded to bf16, sums and states are fp32.
  * Everything else runs on CUDA cores in fp32.  A NaN or infinity in a token
- * reaches that token's and later outputs of its sequence and, since the masked
- * scores are zeros that are multiplied, earlier ones of the same 128 tokens;
- * it never reaches another sequence.  (Padding that may hold such values goes
- * outside the sequences, see packed.)  Asynchronous on `stream`. */
+ * reaches that token's and later outputs of its sequence, no earlier ones and
+ * no other sequence's.  Asynchronous on `stream`. */
 ssd_status ssd_linear_attention(const ssd_linear_shape* shape, const void* q, const ssd_strides* q_strides,
                                 const void* k, const ssd_strides* k_strides, const void* v,
                                 const ssd_strides* v_strides, const float* decay, const int* cu_seqlens,

@@ -175,6 +175,19 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(const ScanLaunch p,
             for (int r = 0; r < 2; ++r) {
                 const int i1 = i0 + r;
                 if (i1 >= n) continue;
+                // a masked score is a zero, but 0 v of an infinity or NaN is one: then only
+                // the causal side again
+                float zero = 0.f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) zero = fmaf(intra[r][q], 0.f, zero);
+                if (!(zero == 0.f)) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) intra[r][q] = 0.f;
+                    for (int j = R.reverse ? i1 : 0; j < (R.reverse ? n : i1 + 1); ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            intra[r][q] = fmaf(sP[i1 * (kC + 4) + j], sV[j * kVT + cg + q], intra[r][q]);
+                }
                 const float e = sTab[(R.reverse ? n - 1 - i1 : i1) + off];
                 const long long row = (long long)it.batch * rows + it.row0 + ct + i1;
                 const long long at = (row * H + it.head) * V + v0 + cg;

@@ -39,6 +39,8 @@
 //
 // With V = 128 the lanes of Z are the state's columns (v), else its rows (k): an
 // MMA takes 128 rows, and the other order would waste half of them.
+#include <climits>
+
 #include "../common.cuh"
 #include "../debug_checks.cuh"
 #include "../linear.h"
@@ -66,7 +68,7 @@ struct __align__(8) Bars {
     // by group of the chunk, not by buffer: a warp then waits for every phase of a
     // barrier that it waits on
     uint64_t x_full[kGroups], x_free[kGroups], clean;
-    uint64_t z_full[2], z_free[2], h_full, h_free, staged, stored;
+    uint64_t z_full[2], z_free[2], h_full, h_free, staged, stored, landed;
     uint64_t done, z_done, s_done;
 };
 
@@ -175,6 +177,69 @@ __device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
+// A masked place of P is a zero, but its product with an infinity or NaN of v is a
+// NaN, which no earlier token's output may see.  Where P V is not finite in
+// some of a warp's 32 rows of a column, the rows are stored without it and the column's
+// `first` keeps the chunk; at the end of the item this adds the causal side's
+// products to them, on CUDA cores (some 100 us; rare).  A later chunk's such rows of
+// the column need none of it: from there on the state's column is not finite, and so
+// is every output.  A warp mends its own rows (lane's: lr) and 32 columns from col,
+// lane l holding column l's chunk.
+__device__ __forceinline__ void mend_rows(const ScanLaunch& s, const ScanItem& it, int nch, int lr, int first,
+                                          const float* table, int col) {
+    const ScanRole& R = s.role[it.role];
+    const bool rev = R.reverse != 0;
+    while (true) {
+        const int c = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
+        if (c == INT_MAX) break;
+        const uint32_t mine = __ballot_sync(0xffffffffu, first == c);  // the columns whose chunk it is
+        if (first == c) first = INT_MAX;
+        const int t = it.t0 + (rev ? nch - 1 - c : c) * kBlk, n = min(kBlk, it.t1 - t);
+        const long long row0 = it.row0 + t;
+        const float* near = table + (rev ? 32 : kBlk - 1) - lr;
+        for (int x = 0; lr < n && x < 32; x += 16) {
+            const uint32_t m = (mine >> x) & 0xffffu;
+            if (m == 0) continue;
+            const __nv_bfloat16* q = (const __nv_bfloat16*)R.q.p + it.batch * R.q.batch + (row0 + lr) * R.q.token +
+                                     it.head / R.q.share * R.q.head;
+            const __nv_bfloat16* k = (const __nv_bfloat16*)R.k.p + it.batch * R.k.batch + row0 * R.k.token +
+                                     it.head / R.k.share * R.k.head;
+            const __nv_bfloat16* v = (const __nv_bfloat16*)R.v.p + it.batch * R.v.batch + row0 * R.v.token +
+                                     it.head / R.v.share * R.v.head + col + x;
+            float a[16] = {};
+#pragma unroll 1
+            for (int j = rev ? lr : 0; j < (rev ? n : lr + 1); ++j) {
+                float sc = 0.f;
+#pragma unroll 1
+                for (int e = 0; e < R.K; ++e) sc = fmaf(to_f32(q[e]), to_f32(k[j * R.k.token + e]), sc);
+                const float p = to_f32(from_f32<__nv_bfloat16>(sc * near[j]));
+                bool done = true;  // nothing finite is left where all are NaN
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if ((m >> e) & 1 && col + x + e < R.V) {
+                        a[e] = fmaf(p, to_f32(v[j * R.v.token + e]), a[e]);
+                        done = done && a[e] != a[e];
+                    }
+                if (done) break;
+            }
+            const long long at = (((long long)it.batch * s.plan.T + row0 + lr) * s.plan.H + it.head) * R.V + col + x;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                if (!((m >> e) & 1) || col + x + e >= R.V ||
+                    !SSD_INB(at + e, (s.plan.packed ? 1LL : s.plan.B) * s.plan.T * s.plan.H * R.V))
+                    continue;
+                if (R.out_f32) {
+                    ((float*)R.out)[at + e] += a[e];
+                } else {
+                    __nv_bfloat16* y = (__nv_bfloat16*)R.out + at + e;
+                    *y = from_f32<__nv_bfloat16>(to_f32(*y) + a[e]);
+                }
+            }
+        }
+        __syncwarp();
+    }
+}
+
 template <int KP, int VP, bool kOut, int kPieces>
 __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ TcParams p) {
     using L = Layout<KP, VP, kOut, kPieces>;
@@ -190,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     float2* sDec = reinterpret_cast<float2*>(sm + L::OFF_DEC);
     Bars* bars = reinterpret_cast<Bars*>(sm + L::OFF_BAR);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::OFF_MISC);
+    volatile uint32_t* sMend = sTmem + 1;  // whether rows are to be mended
     ScanItem* sItem = reinterpret_cast<ScanItem*>(sm + L::OFF_ITEM);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -257,6 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         tc::mbar_init(&bars->h_free, 1);
         tc::mbar_init(&bars->staged, kStateWarps);
         tc::mbar_init(&bars->stored, 1);
+        tc::mbar_init(&bars->landed, 1);
+        *sMend = 0;
         tc::mbar_init(&bars->z_done, 1);
         tc::mbar_init(&bars->s_done, 1);
         tc::mbar_init(&bars->done, 1);
@@ -357,6 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 }
                 if (L::kRing) tc::mbar_arrive(&bars->empty[bv.i]);
                 tc::mbar_arrive(&bars->stored);
+            }
+            if (ok && *sMend) {
+                tc::bulk_wait<0>();
+                tc::mbar_arrive(&bars->landed);
             }
             if (!ok) fail();
         }
@@ -659,6 +731,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars->h_full);
         };
+        // the chunk whose rows of the warp's columns lane, lane + 32 are to be mended
+        int first[VP / 64];
+#pragma unroll
+        for (int e = 0; e < VP / 64; ++e) first[e] = INT_MAX;
         if (kOut && nch > 0) put_h();
         int off = off0;
         bool ok = true;
@@ -713,13 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     ok = wait_warp(&bars->stored, (c - 1) & 1);
                     if (!ok) break;
                 }
-#pragma unroll 1
-                for (int x = 0; x < VP / 32; ++x) {
-                    const int col = half * (VP / 2) + 16 * x;
-                    float a[16], b[16];
-                    tc::tmem_ld16(tl + L::COL_O1 + col, a);
-                    tc::tmem_ld16(tl + L::COL_O2 + col, b);
-                    tc::tmem_ld_wait();
+                auto finish = [&](int col, float (&a)[16], const float (&b)[16]) {
 #pragma unroll
                     for (int q = 0; q < 16; q += 2) {
                         const float2 y = tc::fma2(make_float2(e, e), make_float2(b[q], b[q + 1]), make_float2(a[q], a[q + 1]));
@@ -750,6 +820,45 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                                     make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                             }
                         }
+                    }
+                };
+                float2 zero = make_float2(0.f, 0.f);  // stays so while P V is finite
+#pragma unroll 1
+                for (int x = 0; x < VP / 32; ++x) {
+                    const int col = half * (VP / 2) + 16 * x;
+                    float a[16], b[16];
+                    tc::tmem_ld16(tl + L::COL_O1 + col, a);
+                    tc::tmem_ld16(tl + L::COL_O2 + col, b);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 16; q += 2)
+                        zero = tc::fma2(make_float2(a[q], a[q + 1]), make_float2(0.f, 0.f), zero);
+                    finish(col, a, b);
+                }
+                if (__any_sync(0xffffffffu, lr < n && !(zero.x + zero.y == 0.f))) {  // again: see mend_rows
+#pragma unroll 1
+                    for (int x = 0; x < VP / 32; ++x) {
+                        const int col = half * (VP / 2) + 16 * x;
+                        float a[16], b[16];
+                        tc::tmem_ld16(tl + L::COL_O1 + col, a);
+                        tc::tmem_ld16(tl + L::COL_O2 + col, b);
+                        tc::tmem_ld_wait();
+                        const bool high = VP == 128 && x >= 2;
+                        const uint32_t open =
+                            __ballot_sync(0xffffffffu, (high ? first[VP / 64 - 1] : first[0]) == INT_MAX) >> (16 * (x & 1));
+                        uint32_t now = 0;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            if (__any_sync(0xffffffffu, lr < n && !(a[q] * 0.f == 0.f)) && (open >> q) & 1) {
+                                a[q] = 0.f;
+                                now |= 1u << q;
+                            }
+                        if ((now >> (lane & 15)) & 1 && lane >> 4 == (x & 1)) {
+                            if (high) first[VP / 64 - 1] = c;
+                            else first[0] = c;
+                            *sMend = 1;
+                        }
+                        finish(col, a, b);
                     }
                 }
                 tc::tc_fence_before();
@@ -790,6 +899,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                             make_float4(h[c] * mul, h[c + 1] * mul, h[c + 2] * mul, h[c + 3] * mul);
             }
         }
+        if (kOut && ok && *sMend && wait_warp(&bars->landed, 0))
+#pragma unroll
+            for (int e = 0; e < VP / 64; ++e)
+                mend_rows(p.s, it, nch, lr, first[e], sNear, half * (VP / 2) + 32 * e);
     }
     tc::tc_fence_before();
     __syncthreads();

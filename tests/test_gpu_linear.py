@@ -425,3 +425,35 @@ def test_refusals_on_the_gpu():
         ssd.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], decay, c["init"].transpose(2, 3))
     torch.cuda.synchronize()
     assert torch.equal(ssd.linear_attention(q, k, v, decay)[0], ok)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype,K,V", [(BF, 128, 64), (BF, 64, 128), (BF, 128, 128), (BF, 40, 56), (F32, 64, 64),
+                                       (F32, 20, 70)])
+def test_later_tokens_reach_no_earlier_ones(dtype, K, V, bad):
+    """Infinities and NaN from token 40, and from token 300, on (a batch's padding, say):
+    outputs before them are those without, and gradients where dy is spoiled only
+    before a token are those without behind it."""
+    B, T, H, G = 3, 333, 4, 2
+    c = make(dtype, [0, T, 2 * T, 3 * T], B * T, H, G, K, V)
+    r = {n: c[n].view(B, T, *c[n].shape[1:]).clone() for n in ("q", "k", "v", "dy")}
+    args = (c["q"], c["k"], c["v"], c["decay"], K ** -0.5, c["init"], [0, T, 2 * T, 3 * T], c["dy"], c["dfinal"])
+    ref, size = reference(*args), reference(*args, magnitude=True)
+    for n in ("q", "k", "v"):
+        r[n][0, 40:] = bad
+        r[n][1, 300:] = bad
+    r["v"][2, 200] = bad  # one token's values alone
+    y, _ = ssd.linear_attention(r["q"], r["k"], r["v"], c["decay"], initial_state=c["init"])
+    y = y.clone()
+    for b, first in ((0, 40), (1, 300), (2, 200)):
+        assert not bool(torch.isfinite(y[b, first:]).all())
+        ref["y"].view(B, T, H, V)[b, first:] = float("nan")  # checked above
+    check({"y": y.flatten(0, 1)}, ref, size, dtype, K, V, T, on_tensor_cores(dtype, K, V))
+    clean = {n: c[n].view(B, T, *c[n].shape[1:]) for n in ("q", "k", "v", "dy")}
+    clean["dy"] = clean["dy"].clone()
+    clean["dy"][0, :250] = bad
+    g = ssd.linear_attention_backward(clean["q"], clean["k"], clean["v"], c["decay"], clean["dy"],
+                                      initial_state=c["init"], dfinal=c["dfinal"])
+    for n, d in (("dk", K), ("dv", V)):
+        ref[n].view(B, T, G, d)[0, :250] = float("nan")
+    check({n: g[n].flatten(0, 1) for n in ("dk", "dv")}, ref, size, dtype, K, V, T, on_tensor_cores(dtype, K, V))
