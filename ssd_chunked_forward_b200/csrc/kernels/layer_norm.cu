@@ -223,7 +223,7 @@ __device__ __forceinline__ void team_sum(float (&a)[N], int team, float (*buf)[3
 // two; the division and root that round exactly are forty instructions)
 __device__ __forceinline__ float inv_sqrt(float x) {
     const float r = rsqrtf(x);
-    return r * fmaf(-0.5f * x * r, r, 1.5f);
+    return r > 0.f ? r * fmaf(-0.5f * x * r, r, 1.5f) : r;  // (squares that overflow: 0)
 }
 
 // The rows of a thread: row0, row0 + step, ..  Indices are counted in 32 bits and

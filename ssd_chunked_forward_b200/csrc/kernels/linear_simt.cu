@@ -85,15 +85,15 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(const ScanLaunch p,
     const long long chains = (long long)p.plan.B * H;
 
     // the state entering the item
-    const bool from_init = it.seg == 0;
+    const bool from_init = it.slot_prev < 0;
     for (int e = tid; e < L.K4 * kVT; e += kThreads) {
         const int k = e / kVT, c = e % kVT;
         float h = 0.f;
         if (kOut && k < K && c < vn) {
-            if (!from_init) {
+            if (!from_init && (it.seg > 0 || R.init)) {
                 const long long at = it.slot_prev * K * V + (long long)k * V + v0 + c;
                 if (SSD_INB(at, p.plan.slots() * K * V)) h = p.states[at];
-            } else if (R.init) {
+            } else if (from_init && R.init) {
                 const long long at = chain * K * V + k * R.init_k + (v0 + c) * R.init_v;
                 if (SSD_INB(at, chains * K * V)) h = R.init[at] * R.init_scale;
             }
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(const ScanLaunch p,
         sH[e] = h;
     }
     // a backward scan's initial state meets its first token undecayed
-    int off = (from_init && R.reverse) ? 0 : 1;
+    int off = (it.seg == 0 && R.reverse) ? 0 : 1;
     const int span = it.t1 - it.t0, nch = (span + kC - 1) / kC;
     const float2 full = decay_power(la, kC);
     const int cg = (tid & 15) * 4;  // 4 columns
@@ -323,6 +323,13 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, i
                 const long long at = chain * KV + (e / V) * R.init_k + (e % V) * R.init_v;
                 if (SSD_INB(at, (long long)p.plan.B * p.plan.H * KV)) h[u] = R.init[at] * R.init_scale;
             }
+        }
+        const long long last = it.slot + (it.nseg - 1) * step;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = e0 + u * apart;
+            const long long at = last * KV + e;
+            if (R.init && e < KV && last < p.plan.slots() && SSD_INB(at, p.plan.slots() * KV)) p.states[at] = h[u];
         }
         for (int i = 0; i + 1 < it.nseg; ++i) {
             const long long slot = it.slot + i * step;

@@ -684,14 +684,14 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         const bool holds = kLaneV || lr < KP;  // K = 64: lanes behind it hold nothing
         const uint32_t tl = tmem + ((uint32_t)(quad * 32) << 16);
         float h[CH];
-        const bool from_init = it.seg == 0;
+        const bool from_init = it.slot_prev < 0;
         // element of column c: (k, v)
         auto k_of = [&](int c) -> int { return kLaneV ? c0 + c : lr; };
         auto v_of = [&](int c) -> int { return kLaneV ? lr : c0 + c; };
 #pragma unroll
         for (int c = 0; c < CH; ++c) h[c] = 0.f;
         if (kOut && !from_init) wait_for_earlier();
-        if (kOut && holds && (!from_init || R.init)) {
+        if (kOut && holds && (it.seg > 0 || R.init)) {
             const float* src = from_init ? R.init + chain * K * V : p.s.states + it.slot_prev * K * V;
             const long long sk = from_init ? R.init_k : V, sv = from_init ? R.init_v : 1;
             const float mul = from_init ? R.init_scale : 1.f;

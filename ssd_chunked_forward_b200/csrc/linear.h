@@ -87,7 +87,10 @@ struct ScanItem {
     int batch;              // batch coordinate (0 when packed)
     int len;                // tokens of the sequence
     int t0, t1;             // this item's tokens [t0, t1) of the sequence
-    long long slot, slot_prev;  // states: own, and the one this item starts from (-1: the chain's initial state)
+    // states: own, and the one this item starts from.  A cut chain's first item starts
+    // from its last one's slot, where the initial state is put (it may be read late, when
+    // the final state, which may be the same memory, is written); -1: not cut
+    long long slot, slot_prev;
     int valid;
 };
 
@@ -121,7 +124,7 @@ __device__ inline ScanItem scan_item(const ScanPlan& p, long long it) {
         r.len = p.T;
         r.seg = seg;
         r.nseg = nseg;
-        r.slot_prev = seg > 0 ? r.slot - 1 : -1;
+        r.slot_prev = seg > 0 ? r.slot - 1 : nseg > 1 ? r.slot + nseg - 1 : -1;
         r.valid = 1;
     } else {
         const int lane = threadIdx.x & 31;
@@ -162,7 +165,8 @@ __device__ inline ScanItem scan_item(const ScanPlan& p, long long it) {
         }
         if (!found) return r;
         r.slot = it;
-        r.slot_prev = r.seg > 0 ? it - HR : -1;
+        r.slot_prev = r.seg > 0 ? it - HR : r.nseg > 1 ? it + (long long)(r.nseg - 1) * HR : -1;
+        if (r.slot_prev >= p.items) return r;
         r.valid = 1;
     }
     return r;

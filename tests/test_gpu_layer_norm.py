@@ -153,3 +153,51 @@ def test_autograd_and_differences():
     slope = float((f(1e-5) - f(-1e-5)) / 2e-5)
     along = float(sum((a.double() * u).sum() for a, u in zip(got, d)))
     assert abs(slope - along) <= 1e-5 * sum(float(a.double().norm() * u.norm()) for a, u in zip(got, d))
+
+
+@pytest.mark.parametrize("dtype,rows,width,groups,gate", [(BF, 32768, 5120, 80, True), (BF, 50000, 640, 1, False),
+                                                          (F32, 9000, 2048, 16, True), (BF, 70001, 24, 1, True)])
+def test_rows_do_not_know_of_each_other(dtype, rows, width, groups, gate):
+    """Many rows (blocks take several turns, threads many rows): each row's results are
+    to the bit those of a call with a few of them, whatever the others hold."""
+    c = make(dtype, rows, width, gate)
+    c["x"][7::1000] = float("nan")
+    c["dy"][11::1000] = float("inf")
+    y, stats = ssd.layer_norm(c["x"], c["weight"], c["bias"], groups=groups, gate=c["gate"])
+    g = ssd.layer_norm_backward(c["x"], c["weight"], c["bias"], c["dy"], stats, groups=groups, gate=c["gate"])
+    for a in (0, 1, rows // 2, rows - 5):
+        s = slice(a, a + 5)
+        part = {n: None if c[n] is None else c[n][s] for n in ("x", "gate", "dy")}
+        y2, stats2 = ssd.layer_norm(part["x"], c["weight"], c["bias"], groups=groups, gate=part["gate"])
+        g2 = ssd.layer_norm_backward(part["x"], c["weight"], c["bias"], part["dy"], stats2, groups=groups,
+                                     gate=part["gate"])
+        same = lambda p, q: torch.equal(torch.nan_to_num(p), torch.nan_to_num(q))  # noqa: E731
+        assert same(y[s], y2) and same(stats[s], stats2) and same(g["dx"][s], g2["dx"])
+        assert gate is False or same(g["dgate"][s], g2["dgate"])
+    fine = torch.ones(rows, dtype=torch.bool, device="cuda")
+    fine[7::1000] = False
+    assert bool(torch.isfinite(y[fine]).all())
+
+
+def test_refusals_on_the_gpu():
+    """Wrong types, shapes, devices and layouts are errors of the call."""
+    c = make(BF, 12, 64, True)
+    x, w, b, z = c["x"], c["weight"], c["bias"], c["gate"]
+    ok, stats = ssd.layer_norm(x, w, b, groups=2, gate=z)
+    for bad in [dict(x=x.half()), dict(weight=w.double()), dict(weight=w[:32]), dict(bias=b.cpu()), dict(gate=z.float()),
+                dict(gate=z[:6]), dict(groups=5), dict(groups=0), dict(x=x.t()), dict(x=x[:0], gate=z[:0]),
+                dict(y=ok.float()), dict(y=ok[:6]), dict(eps=float("nan")), dict(eps=-1.0)]:
+        with pytest.raises((ValueError, ssd.SSDError)):
+            ssd.layer_norm(**{**dict(x=x, weight=w, bias=b, groups=2, gate=z), **bad})
+    for bad in [dict(dy=c["dy"].float()), dict(stats=stats[:6]), dict(stats=stats.double()), dict(dy=c["dy"].cpu())]:
+        with pytest.raises((ValueError, ssd.SSDError)):
+            ssd.layer_norm_backward(**{**dict(x=x, weight=w, bias=b, dy=c["dy"], stats=stats, groups=2, gate=z), **bad})
+    torch.cuda.synchronize()
+    assert torch.equal(ssd.layer_norm(x, w, b, groups=2, gate=z)[0], ok)
+
+
+def test_squares_that_overflow():
+    """Numbers whose squares leave fp32: rstd is 0, as the formula in fp32 has it, not NaN."""
+    x = torch.randn(3, 256, device="cuda") * 1e25
+    y, stats = ssd.layer_norm(x, None, None)
+    assert bool((stats[..., 1] == 0).all()) and bool((y == 0).all())

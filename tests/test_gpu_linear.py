@@ -457,3 +457,20 @@ def test_later_tokens_reach_no_earlier_ones(dtype, K, V, bad):
     for n, d in (("dk", K), ("dv", V)):
         ref[n].view(B, T, G, d)[0, :250] = float("nan")
     check({n: g[n].flatten(0, 1) for n in ("dk", "dv")}, ref, size, dtype, K, V, T, on_tensor_cores(dtype, K, V))
+
+
+@pytest.mark.parametrize("dtype,K,V,packed", [(BF, 128, 64, False), (BF, 128, 128, True), (F32, 20, 24, False),
+                                              (F32, 20, 24, True)])
+def test_cut_chains_update_the_state_in_place(dtype, K, V, packed):
+    """final_state is initial_state, in chains that are cut into items: the first item
+    starts from what the state held."""
+    T = 3000
+    c = make(dtype, [0, T], T, 2, 2, K, V)
+    e = (lambda t: t) if packed else (lambda t: t[None])
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda") if packed else None
+    y, final = ssd.linear_attention(e(c["q"]), e(c["k"]), e(c["v"]), c["decay"], initial_state=c["init"], cu_seqlens=cu)
+    for _ in range(3):
+        state = c["init"].clone()
+        y2, _ = ssd.linear_attention(e(c["q"]), e(c["k"]), e(c["v"]), c["decay"], initial_state=state,
+                                     final_state=state, cu_seqlens=cu)
+        assert torch.equal(y2, y) and torch.equal(state, final)
