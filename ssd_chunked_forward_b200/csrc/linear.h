@@ -48,7 +48,7 @@ struct ScanRole {
 };
 
 constexpr int kScanRoles = 3;
-constexpr int kScanChunk = 128;  // segment bounds are multiples of this many tokens
+constexpr int kScanChunk = 128;  // tokens of a chunk on tensor cores
 
 // How the chains (sequence, head, role) are cut into items, one per block.
 // Rows of equal length ([B][T]): the first `nfull` chains are one item each,

@@ -37,10 +37,10 @@ int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 // nseg items each where that is shorter, although a cut chain's k and v are
 // read twice (state-only items first: about 0.6 of a full item's time).
 // `start`, `launches`: an item's start and the two further launches, in units
-// of one 128-token chunk.
-void plan_rows(ScanPlan& p, int at_once, double start, double launches) {
+// of one chunk.
+void plan_rows(ScanPlan& p, int at_once, int chunk, double start, double launches) {
     const long long chains = (long long)p.B * p.H * p.nroles;
-    const int nch = cdiv(p.T, ssd::kScanChunk);
+    const int nch = cdiv(p.T, chunk);
     const long long left = chains % at_once;
     int best = 1;
     double cost = nch + start;
@@ -63,7 +63,7 @@ void plan_rows(ScanPlan& p, int at_once, double start, double launches) {
         return;
     }
     const int per = cdiv(nch, best);
-    p.seg_tokens = per * ssd::kScanChunk;
+    p.seg_tokens = per * chunk;
     p.nseg = cdiv(nch, per);
     p.nfull = (int)(chains - left);
     p.items = p.nfull + left * p.nseg;
@@ -72,10 +72,10 @@ void plan_rows(ScanPlan& p, int at_once, double start, double launches) {
 // Packed sequences: their lengths are on the device, so every sequence is cut
 // at the same distance, which gives about three items for each that runs at a
 // time if the tokens are spread evenly, and never less than four chunks.
-void plan_packed(ScanPlan& p, int at_once, const int* cu) {
+void plan_packed(ScanPlan& p, int at_once, int chunk, const int* cu) {
     const long long all = (long long)p.T * p.H * p.nroles;
-    long long seg = all / (3LL * at_once) / ssd::kScanChunk * ssd::kScanChunk;
-    if (seg < 4 * ssd::kScanChunk) seg = 4 * ssd::kScanChunk;
+    long long seg = all / (3LL * at_once) / chunk * chunk;
+    if (seg < 4 * chunk) seg = 4 * chunk;
     if (seg > (1 << 30)) seg = 1 << 30;
     p.packed = 1;
     p.cu = cu;
@@ -94,9 +94,13 @@ ScanPlan make_plan(const ssd_linear_shape& s, int nroles, int vmax, bool tc, con
     // tensor cores: one block per SM; CUDA cores: two, of 64 state columns each
     const int tiles = cdiv(vmax, 64);
     int at_once = tc ? kSMs : 2 * kSMs / tiles;
-    if (s.packed) plan_packed(p, at_once, cu);
-    else if (tc) plan_rows(p, at_once, 1.5, 3.0);
-    else plan_rows(p, at_once, 0.3, 0.5);
+    // (CUDA cores: bounds every 128 tokens instead of 32 cost 52 against 33 us for 2 x 333
+    // tokens of 8 heads; without the states' size in an item's start the gradients of 1 x 300
+    // tokens, 24 heads, 128 x 128 took 173 us instead of 131)
+    constexpr int kSimtChunk = 32;
+    if (s.packed) plan_packed(p, at_once, tc ? ssd::kScanChunk : kSimtChunk, cu);
+    else if (tc) plan_rows(p, at_once, ssd::kScanChunk, 1.5, 3.0);
+    else plan_rows(p, at_once, kSimtChunk, 0.5 * s.K * s.V / 4096.0, 1.0);
     return p;
 }
 
