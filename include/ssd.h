@@ -434,6 +434,7 @@ size_t ssd_backward_workspace_size(const ssd_shape* shape);
  *   decay [H] fp32 log-decays (<= 0 assumed, not checked)
  *   y [B][T][H][V] dtype, contiguous
  *   states [B][H][K][V] fp32, contiguous: the layout of ssd_forward's states
+ *   y, the gradients and the states start on 16-byte boundaries
  * packed != 0: the tensors have no batch dimension ([T][heads][d]); sequence s
  * of the B sequences is the rows cu_seqlens[s] <= t < cu_seqlens[s+1]
  * (cu_seqlens [B+1] int32 on the device, never decreasing, within [0, T];

@@ -59,8 +59,20 @@ def ssd_autograd(x, a, Bm, Cm, D=None, chunk=256, initial_state=None, *, ops=Non
     return SSDFunction.apply(x, a, Bm, Cm, D, initial_state, chunk, ops or _Ops)
 
 
+def _aligned(t):
+    """t contiguous and on a 16-byte boundary."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _LinearOps:
-    forward = staticmethod(ssd.linear_attention)
+    @staticmethod
+    def forward(q, k, v, decay, *, scale, initial_state, cu_seqlens):
+        # rows of no sequence: zero, so that what follows in a graph can take all rows
+        y = None if cu_seqlens is None else q.new_zeros(q.shape[:-1] + v.shape[-1:])
+        return ssd.linear_attention(q, k, v, decay, scale=scale, initial_state=initial_state, cu_seqlens=cu_seqlens,
+                                    y=y)
+
     backward = staticmethod(ssd.linear_attention_backward)
 
 
@@ -80,8 +92,8 @@ class LinearAttentionFunction(torch.autograd.Function):
         if dy is None:
             dy = q.new_zeros(q.shape[:-1] + v.shape[-1:])
         want = init is not None and ctx.needs_input_grad[4]
-        g = ctx.ops.backward(q, k, v, decay, dy.contiguous(), scale=ctx.scale, initial_state=init,
-                             dfinal=None if dfinal is None else dfinal.contiguous(), cu_seqlens=cu, want_dinit=want)
+        g = ctx.ops.backward(q, k, v, decay, _aligned(dy), scale=ctx.scale, initial_state=init,
+                             dfinal=None if dfinal is None else _aligned(dfinal), cu_seqlens=cu, want_dinit=want)
         return g["dq"], g["dk"], g["dv"], None, g["dinit"] if want else None, None, None, None
 
 
@@ -89,7 +101,8 @@ def linear_attention_autograd(q, k, v, decay, *, scale=None, initial_state=None,
     """(y, final_state) of ssd.linear_attention as a differentiable torch
     operation; gradients flow to q, k, v and initial_state.  The decay is a
     constant of the layer: one that requires a gradient is refused (a learned
-    log-decay per token is what ssd_autograd takes)."""
+    log-decay per token is what ssd_autograd takes).  Rows outside every packed
+    sequence are zero, in y and in the gradients."""
     if decay.requires_grad:
         raise ValueError("decay has no gradient here; use ssd_autograd for a learned decay")
     return LinearAttentionFunction.apply(q, k, v, decay, initial_state, cu_seqlens, scale, ops or _LinearOps)

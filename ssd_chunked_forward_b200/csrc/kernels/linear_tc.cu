@@ -235,10 +235,11 @@ __device__ __forceinline__ void mend_rows(const ScanLaunch& s, const ScanItem& i
                     !SSD_INB(at + e, (s.plan.packed ? 1LL : s.plan.B) * s.plan.T * s.plan.H * R.V))
                     continue;
                 if (R.out_f32) {
-                    ((float*)R.out)[at + e] += a[e];
+                    float* y = (float*)R.out + at + e;
+                    *y = __ldcg(y) + a[e];
                 } else {
                     __nv_bfloat16* y = (__nv_bfloat16*)R.out + at + e;
-                    *y = from_f32<__nv_bfloat16>(to_f32(*y) + a[e]);
+                    *y = from_f32<__nv_bfloat16>(to_f32(__ldcg(y)) + a[e]);  // (not an L1 line of before)
                 }
             }
         }
@@ -855,7 +856,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         uint32_t now = 0;
 #pragma unroll
                         for (int q = 0; q < 16; ++q)
-                            if (__any_sync(0xffffffffu, lr < n && !(a[q] * 0.f == 0.f)) && (open >> q) & 1) {
+                            // (not rows whose q is what is not finite: there Q H is not either)
+                            if (__any_sync(0xffffffffu, lr < n && !(a[q] * 0.f == 0.f) && b[q] * 0.f == 0.f) &&
+                                (open >> q) & 1) {
                                 a[q] = 0.f;
                                 now |= 1u << q;
                             }

@@ -661,7 +661,8 @@ def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqle
     contiguous), decay [H] float32 log-decays, initial_state [B,H,K,V] float32
     or None (zero), scale (None: K**-0.5).  With cu_seqlens (int32 [S+1], on the device) the
     tensors are [T,heads,d] with S sequences one behind the other, the states
-    [S,H,K,V]; rows of a given y outside every sequence stay as they are.
+    [S,H,K,V]; rows of a given y outside every sequence stay as they are (those
+    of a new y are not set).
     Returns y [B,T,H,V] and the state [B,H,K,V] float32 (None with
     want_final=False).  Asynchronous on the current stream of q's device."""
     plan, dev = _linear_plan(q, k, v, decay, cu_seqlens), q.device

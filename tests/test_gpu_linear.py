@@ -474,3 +474,39 @@ def test_cut_chains_update_the_state_in_place(dtype, K, V, packed):
         y2, _ = ssd.linear_attention(e(c["q"]), e(c["k"]), e(c["v"]), c["decay"], initial_state=state,
                                      final_state=state, cu_seqlens=cu)
         assert torch.equal(y2, y) and torch.equal(state, final)
+
+
+def test_autograd_of_packed_rows_and_unaligned_gradients():
+    """Rows of no sequence are zero in y and in the gradients; a gradient that starts off
+    a 16-byte boundary is taken."""
+    cuts, total, H, K, V = [4, 60, 200], 230, 2, 64, 64
+    c = make(BF, cuts, total, H, H, K, V, outside=float("nan"))
+    cu = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    q, k, v = (c[n].requires_grad_() for n in "qkv")
+    y, _ = linear_attention_autograd(q, k, v, c["decay"], initial_state=c["init"], cu_seqlens=cu)
+    assert bool((y[:4] == 0).all()) and bool((y[200:] == 0).all()) and bool(torch.isfinite(y).all())
+    dy = torch.empty(total * H * V + 1, dtype=BF, device="cuda")[1:].view(total, H, V).copy_(c["dy"])
+    assert dy.data_ptr() % 16 != 0
+    got = torch.autograd.grad(y, [q, k, v], dy)
+    want = ssd.linear_attention_backward(q.detach(), k.detach(), v.detach(), c["decay"], c["dy"], cu_seqlens=cu,
+                                         initial_state=c["init"], want_dinit=False)
+    for t, n in zip(got, ("dq", "dk", "dv")):
+        assert torch.equal(t, want[n]) and bool((t[:4] == 0).all()) and bool((t[200:] == 0).all())
+
+
+@pytest.mark.parametrize("dtype,K,V", [(BF, 128, 64), (BF, 128, 128), (F32, 64, 64)])
+def test_spoiled_queries_hide_nothing(dtype, K, V):
+    """Queries that are not finite spoil their own outputs only, and values that are not,
+    behind them in the sequence, still no earlier output."""
+    T, H = 400, 2
+    c = make(dtype, [0, T], T, H, H, K, V)
+    args = (c["q"], c["k"], c["v"], c["decay"], K ** -0.5, c["init"], [0, T], c["dy"], c["dfinal"])
+    ref, size = reference(*args), reference(*args, magnitude=True)
+    c["q"][0:64] = float("nan")
+    c["q"][140] = float("inf")
+    c["v"][350:] = float("nan")
+    y, _ = ssd.linear_attention(c["q"][None], c["k"][None], c["v"][None], c["decay"], initial_state=c["init"])
+    for s in (slice(0, 64), slice(140, 141), slice(350, T)):
+        ref["y"][s] = float("nan")
+        assert not bool(torch.isfinite(y[0, s]).any())
+    check({"y": y[0]}, ref, size, dtype, K, V, T, on_tensor_cores(dtype, K, V))
