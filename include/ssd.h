@@ -434,7 +434,8 @@ size_t ssd_backward_workspace_size(const ssd_shape* shape);
  *   decay [H] fp32 log-decays (<= 0 assumed, not checked)
  *   y [B][T][H][V] dtype, contiguous
  *   states [B][H][K][V] fp32, contiguous: the layout of ssd_forward's states
- *   y, the gradients and the states start on 16-byte boundaries
+ *   y, the gradients and the states start on 16-byte boundaries; results must
+ *   not overlap inputs, but for final_state, which may be initial_state
  * packed != 0: the tensors have no batch dimension ([T][heads][d]); sequence s
  * of the B sequences is the rows cu_seqlens[s] <= t < cu_seqlens[s+1]
  * (cu_seqlens [B+1] int32 on the device, never decreasing, within [0, T];
@@ -511,8 +512,8 @@ size_t ssd_linear_backward_workspace_size(const ssd_linear_shape* shape);
  * x [rows][width] dtype with x_stride elements from row to row; gate the same
  * with gate_stride, or NULL (no product); weight, bias [width] fp32 or NULL (1
  * and 0); y [rows][width] dtype, contiguous; stats [rows][groups][2] fp32, mean
- * and rstd, or NULL (not wanted; the backward needs it).  width / groups <=
- * 16384; eps > 0.  Statistics are fp32, the variance taken about the mean. */
+ * and rstd, or NULL (not wanted; the backward needs it).  y may be x itself or
+ * the gate, but not overlap them otherwise.  width / groups <= 16384; eps > 0.  Statistics are fp32, the variance taken about the mean. */
 typedef struct {
     long long rows;
     int width, groups;

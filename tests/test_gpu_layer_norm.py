@@ -201,3 +201,32 @@ def test_squares_that_overflow():
     x = torch.randn(3, 256, device="cuda") * 1e25
     y, stats = ssd.layer_norm(x, None, None)
     assert bool((stats[..., 1] == 0).all()) and bool((y == 0).all())
+
+
+@pytest.mark.parametrize("dtype,rows,width,groups", [(BF, 5000, 2560, 1), (BF, 3000, 1536, 24), (F32, 700, 455, 1),
+                                                     (BF, 900, 455, 1)])
+def test_in_place(dtype, rows, width, groups):
+    """y may be x itself, or the gate."""
+    c = make(dtype, rows, width, True)
+    want, stats = ssd.layer_norm(c["x"], c["weight"], c["bias"], groups=groups, gate=c["gate"])
+    for n in ("x", "gate"):
+        t = {m: c[m].clone() for m in ("x", "gate")}
+        y, s2 = ssd.layer_norm(t["x"], c["weight"], c["bias"], groups=groups, gate=t["gate"], y=t[n])
+        assert y is t[n] and torch.equal(y, want) and torch.equal(s2, stats)
+
+
+def test_two_streams_at_once():
+    """Calls side by side on two streams, gradients among them."""
+    c = make(BF, 6000, 1536, True)
+    want, stats = ssd.layer_norm(c["x"], c["weight"], c["bias"], groups=24, gate=c["gate"])
+    back = lambda s: ssd.layer_norm_backward(c["x"], c["weight"], c["bias"], c["dy"], stats, groups=24,  # noqa: E731
+                                             gate=c["gate"], stream=s)
+    g = back(None)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(10):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(back(None))
+    torch.cuda.synchronize()
+    for r in got:
+        assert all(torch.equal(r[n], g[n]) for n in g)
