@@ -189,10 +189,11 @@ __device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity) {
 // `first` keeps the chunk; at the end of the item this adds the causal side's
 // products to them, on CUDA cores (some 100 us; rare).  A later chunk's such rows of
 // the column need none of it: from there on the state's column is not finite, and so
-// is every output.  (Looking for them costs 1.5 % at 128 x 64, 8 % at 64 x 128, nothing
-// measurable at 128 x 128; a vote for every 16 columns instead of one a chunk cost 11 %
-// at 64 x 128, mending at once, which makes registers spill, 25 %.)  A warp mends its own rows (lane's: lr) and 32 columns from col,
+// is every output.  A warp mends its own rows (lane's: lr) and 32 columns from col,
 // lane l holding column l's chunk.
+// Looking for such rows costs 1.5 % at 128 x 64, 8 % at 64 x 128, nothing measurable
+// at 128 x 128; a vote for every 16 columns instead of one a chunk cost 11 % at
+// 64 x 128, mending at once, which makes registers spill, 25 %.
 __device__ __forceinline__ void mend_rows(const ScanLaunch& s, const ScanItem& it, int nch, int lr, int first,
                                           const float* table, int col) {
     const ScanRole& R = s.role[it.role];
