@@ -8,6 +8,8 @@ turns torch tensors into device pointers, the current torch stream into a
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -163,6 +165,48 @@ def _ptr(t):
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _torch_stream(stream, device):
+    """``stream`` (a torch stream, another object with a ``cuda_stream``, or a
+    raw handle) as a torch stream of ``device``."""
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device != device:
+            raise ValueError(f"stream must be on {device}")
+        return stream
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if handle in (0, 1):  # the legacy default stream by its two names
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
+def _on_its_stream(fn):
+    """A call that allocates, with ``stream=s`` as under ``torch.cuda.stream(s)``:
+    what it allocates, clears and copies is queued on s like its kernels, and
+    temporary memory goes back to that stream's pool, whose next user runs behind
+    them.  New results are also marked as used by the caller's own stream, so that
+    dropping them there is safe while it still reads them."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        if len(args) > at:
+            args, stream = args[:at], args[at]
+        else:
+            stream = kw.pop("stream", None)
+        given = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)] if stream is not None else []
+        if not given or not given[0].is_cuda:  # (no CUDA tensor: refused below)
+            return fn(*args, **kw)
+        here, side = torch.cuda.current_stream(given[0].device), _torch_stream(stream, given[0].device)
+        with torch.cuda.stream(side):
+            out = fn(*args, **kw)
+        if side != here:
+            for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+                if t is not None and not any(t is g for g in given):
+                    t.record_stream(here)
+        return out
+
+    return call
 
 
 def _stream(stream):
@@ -530,9 +574,10 @@ def backward(x, a, Bm, Cm, D, dy, chunk=256, *, dfinal=None, initial_state=None,
 # ---- linear attention with a decay for each head, and layer norm -------------
 #
 # These calls run on the device of their tensors, on its current torch stream
-# unless another is given.  A single token's step takes a few microseconds on the
-# GPU, so the host's part is kept short: what follows from the tensors' shapes and
-# strides alone is checked and laid out once for each combination of them.
+# unless another is given, whose order with the inputs is then the caller's.  A
+# single token's step takes a few microseconds on the GPU, so the host's part is
+# kept short: what follows from the tensors' shapes and strides alone is checked
+# and laid out once for each combination of them.
 
 def _on_device(name, t, device, dtype=None, shape=None, contiguous=True):
     if t.device != device or not t.is_cuda:
@@ -553,12 +598,9 @@ def _dtype_code(dtype):
     raise ValueError("tensors must be float32 or bfloat16")
 
 
-def _call(where, device, stream, fn, *args):
-    """fn(*args, stream) with `device` current; raises SSDError."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        stream = _stream(stream)
+def _call(where, device, fn, *args):
+    """fn(*args, device's current stream) with `device` current; raises SSDError."""
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
         code = fn(*args, stream)
     else:
@@ -651,6 +693,7 @@ def linear_backward_workspace_size(shape: LinearShape) -> int:
     return int(load().ssd_linear_backward_workspace_size(ctypes.byref(shape)))
 
 
+@_on_its_stream
 def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqlens=None, y=None, final_state=None,
                      want_final=True, workspace=None, stream=None):
     """y and the final state of linear attention with a decay for each head:
@@ -678,13 +721,14 @@ def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqle
         final_state = torch.empty(plan.state, dtype=torch.float32, device=dev)
     workspace = _workspace_arg(workspace, plan.forward_bytes, dev)
     shape, sq, sk, sv = plan.refs
-    _call("ssd_linear_attention", dev, stream, load().ssd_linear_attention, shape, q.data_ptr(), sq, k.data_ptr(), sk,
+    _call("ssd_linear_attention", dev, load().ssd_linear_attention, shape, q.data_ptr(), sq, k.data_ptr(), sk,
           v.data_ptr(), sv, decay.data_ptr(), _ptr(cu_seqlens), _ptr(initial_state),
           plan.scale if scale is None else scale, y.data_ptr(), _ptr(final_state), workspace.data_ptr(),
           workspace.numel())
     return y, final_state
 
 
+@_on_its_stream
 def linear_attention_step(q, k, v, decay, state, *, scale=None, y=None, stream=None):
     """One token of linear_attention() for a batch of sequences, in place on
     ``state`` [B,H,K,V] float32: q [B,H,K], k [B,G,K], v [B,G,V], decay [H].
@@ -696,12 +740,13 @@ def linear_attention_step(q, k, v, decay, state, *, scale=None, y=None, stream=N
     else:
         _on_device("y", y, dev, q.dtype, plan.y)
     shape, sq, sk, sv = plan.refs
-    _call("ssd_linear_attention_step", dev, stream, load().ssd_linear_attention_step, shape, q.data_ptr(), sq,
+    _call("ssd_linear_attention_step", dev, load().ssd_linear_attention_step, shape, q.data_ptr(), sq,
           k.data_ptr(), sk, v.data_ptr(), sv, decay.data_ptr(), plan.scale if scale is None else scale,
           state.data_ptr(), y.data_ptr())
     return y
 
 
+@_on_its_stream
 def linear_attention_backward(q, k, v, decay, dy, *, scale=None, initial_state=None, dfinal=None, cu_seqlens=None,
                               want_dinit=True, workspace=None, stream=None):
     """Gradients of sum(dy * y) + <dfinal, final_state> of linear_attention()
@@ -719,7 +764,7 @@ def linear_attention_backward(q, k, v, decay, dy, *, scale=None, initial_state=N
     dinit = torch.empty(plan.state, dtype=torch.float32, device=dev) if want_dinit else None
     workspace = _workspace_arg(workspace, plan.backward_bytes, dev)
     shape, sq, sk, sv = plan.refs
-    _call("ssd_linear_attention_backward", dev, stream, load().ssd_linear_attention_backward, shape, q.data_ptr(), sq,
+    _call("ssd_linear_attention_backward", dev, load().ssd_linear_attention_backward, shape, q.data_ptr(), sq,
           k.data_ptr(), sk, v.data_ptr(), sv, decay.data_ptr(), _ptr(cu_seqlens), _ptr(initial_state),
           plan.scale if scale is None else scale, dy.data_ptr(), _ptr(dfinal), dq.data_ptr(), dk.data_ptr(),
           dv.data_ptr(), _ptr(dinit), workspace.data_ptr(), workspace.numel())
@@ -784,6 +829,7 @@ def _norm_plan(x, weight, bias, groups, gate, dy=None):
     return plan
 
 
+@_on_its_stream
 def layer_norm(x, weight=None, bias=None, *, groups=1, gate=None, eps=1e-5, y=None, stream=None):
     """Layer norm over each of the ``groups`` equal parts of x's last dimension
     (groups = heads: the norm behind a sequence mixer), times silu(gate):
@@ -799,11 +845,12 @@ def layer_norm(x, weight=None, bias=None, *, groups=1, gate=None, eps=1e-5, y=No
     else:
         _on_device("y", y, dev, x.dtype, x.shape)
     stats = torch.empty(plan.stats, dtype=torch.float32, device=dev)
-    _call("ssd_layer_norm", dev, stream, load().ssd_layer_norm, plan.shape, x.data_ptr(), plan.x_stride, _ptr(weight),
+    _call("ssd_layer_norm", dev, load().ssd_layer_norm, plan.shape, x.data_ptr(), plan.x_stride, _ptr(weight),
           _ptr(bias), _ptr(gate), plan.gate_stride, eps, y.data_ptr(), stats.data_ptr())
     return y, stats
 
 
+@_on_its_stream
 def layer_norm_backward(x, weight, bias, dy, stats, *, groups=1, gate=None, want_dweight=True, want_dbias=True,
                         workspace=None, stream=None):
     """Gradients of sum(dy * y) of layer_norm() for the same inputs and its
@@ -817,7 +864,7 @@ def layer_norm_backward(x, weight, bias, dy, stats, *, groups=1, gate=None, want
     dbias = torch.empty(plan.width, dtype=torch.float32, device=dev) if want_dbias else None
     if want_dweight or want_dbias:
         workspace = _workspace_arg(workspace, plan.sums_bytes, dev)
-    _call("ssd_layer_norm_backward", dev, stream, load().ssd_layer_norm_backward, plan.shape, x.data_ptr(),
+    _call("ssd_layer_norm_backward", dev, load().ssd_layer_norm_backward, plan.shape, x.data_ptr(),
           plan.x_stride, _ptr(weight), _ptr(bias), _ptr(gate), plan.gate_stride, dy.data_ptr(), plan.dy_stride,
           stats.data_ptr(), dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(dgate), _ptr(workspace),
           0 if workspace is None else workspace.numel())
