@@ -195,8 +195,8 @@ def _on_its_stream(fn):
         else:
             stream = kw.pop("stream", None)
         given = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)] if stream is not None else []
-        if not given or not given[0].is_cuda:  # (no CUDA tensor: refused below)
-            return fn(*args, **kw)
+        if not given or not given[0].is_cuda:  # addresses, or tensors that fn refuses
+            return fn(*args, stream=stream, **kw)
         here, side = torch.cuda.current_stream(given[0].device), _torch_stream(stream, given[0].device)
         with torch.cuda.stream(side):
             out = fn(*args, **kw)
@@ -267,6 +267,7 @@ def _check_inputs(x, a, Bm, Cm, D):
         raise ValueError("D must be a contiguous float32 CUDA tensor")
 
 
+@_on_its_stream
 def forward(x, a, Bm, Cm, D=None, chunk=256, *, y=None, final_state=None, want_final=True,
             workspace=None, path=PATH_AUTO, flags=0, stream=None, initial_state=None):
     """y[B,T,H,P] (and final state [B,H,N,P] fp32) of the chunked SSD forward.
@@ -274,7 +275,8 @@ def forward(x, a, Bm, Cm, D=None, chunk=256, *, y=None, final_state=None, want_f
     x [B,T,H,P], Bm/Cm [B,T,G,N] (float32 or bfloat16, same dtype), a [B,T,H]
     or [B,T,H,N] float32 log-decays, D [H] float32 or None, initial_state
     [B,H,N,P] float32 or None (zero).  Asynchronous on the current torch
-    stream (or ``stream``)."""
+    stream, or on ``stream``, where what it allocates then belongs too; the order
+    of that stream with the inputs is the caller's, as for every call here."""
     _check_inputs(x, a, Bm, Cm, D)
     if initial_state is not None and (initial_state.dtype != torch.float32 or not initial_state.is_cuda
                                       or not initial_state.is_contiguous()):
@@ -336,6 +338,7 @@ def device_status_where(workspace, stream=None):
     return st, line.value, block.value, thread.value
 
 
+@_on_its_stream
 def chunk_cumsum(shape: Shape, a, cum=None, stream=None):
     nc = -(-shape.T // shape.chunk)  # the last chunk may end past T
     if cum is None:
@@ -346,6 +349,7 @@ def chunk_cumsum(shape: Shape, a, cum=None, stream=None):
     return cum
 
 
+@_on_its_stream
 def chunk_state(shape: Shape, x, Bm, cum, states=None, impl=IMPL_AUTO, stream=None):
     nc = -(-shape.T // shape.chunk)  # the last chunk may end past T
     if states is None:
@@ -362,6 +366,7 @@ def state_pass(shape: Shape, cum, states, final_state=None, stream=None):
     return states, final_state
 
 
+@_on_its_stream
 def chunk_scan(shape: Shape, x, Bm, Cm, cum, Hin, D=None, y=None, impl=IMPL_AUTO, stream=None):
     if y is None:
         y = torch.empty_like(x)
@@ -385,6 +390,7 @@ def forward_host(shape: Shape, x_h, a_h, Bm_h, Cm_h, D_h, y_h, final_h, dev_buf,
                                    dev_buf.numel(), _stream(stream)), "ssd_forward_host")
 
 
+@_on_its_stream
 def forward_noalloc(x, a, Bm, Cm, D=None, chunk=256, *, y=None, final_state=None, stream=None):
     """The fused forward with the library's own fixed scratch (no workspace,
     nothing allocated by the library); see ssd_forward_noalloc in ssd.h."""
@@ -402,6 +408,7 @@ def forward_noalloc(x, a, Bm, Cm, D=None, chunk=256, *, y=None, final_state=None
     return y, final_state
 
 
+@_on_its_stream
 def decode_step(x, a, Bm, Cm, D, state, *, y=None, stream=None):
     """One recurrent step for a batch of single tokens, in place on ``state``.
 
@@ -427,6 +434,7 @@ def decode_step(x, a, Bm, Cm, D, state, *, y=None, stream=None):
     return y
 
 
+@_on_its_stream
 def discretize(dt_raw, dt_bias, A_log, x, *, a_out=None, x_out=None, stream=None):
     """dt = softplus(dt_raw + dt_bias); returns (a, x_out): a = -dt exp(A_log)
     ([B,T,H], or [B,T,H,N] when A_log is [H,N]) and x_out = dt x ([B,T,H,P],
@@ -449,6 +457,7 @@ def discretize(dt_raw, dt_bias, A_log, x, *, a_out=None, x_out=None, stream=None
     return a_out, x_out
 
 
+@_on_its_stream
 def forward_discretized(x, dt_raw, dt_bias, A_log, Bm, Cm, D=None, chunk=256, *, y=None, final_state=None,
                         want_final=True, workspace=None, stream=None):
     """discretize() followed by forward() in one fused pass (x_out and a are never
@@ -477,6 +486,7 @@ def forward_discretized(x, dt_raw, dt_bias, A_log, Bm, Cm, D=None, chunk=256, *,
     return y, final_state
 
 
+@_on_its_stream
 def decay_total(a, *, out=None, stream=None):
     """Total log-decay of each chain over the sequence: a [B,T,H] -> [B,H]
     (a [B,T,H,N] -> [B,H,N])."""
@@ -493,6 +503,7 @@ def decay_total(a, *, out=None, stream=None):
     return out
 
 
+@_on_its_stream
 def state_combine(finals, totals, h0=None, *, out=None, stream=None):
     """finals [S,B,H,N,P] (each segment's final state from zero), totals
     [S,B,H] or [S,B,H,N] -> h_in [S+1,B,H,N,P]: h_in[s] enters segment s,
@@ -510,6 +521,7 @@ def state_combine(finals, totals, h0=None, *, out=None, stream=None):
     return out
 
 
+@_on_its_stream
 def segment_state(x, a, Bm, chunk=256, *, final_state=None, total=None, workspace=None, stream=None):
     """The state a segment builds from a zero start, [B,H,N,P] fp32, and its
     total log-decay [B,H] (or [B,H,N]), without computing its outputs."""
@@ -535,6 +547,7 @@ def backward_workspace_size(shape: Shape) -> int:
     return int(load().ssd_backward_workspace_size(ctypes.byref(shape)))
 
 
+@_on_its_stream
 def backward(x, a, Bm, Cm, D, dy, chunk=256, *, dfinal=None, initial_state=None, want_dD=True,
              want_dinit=True, workspace=None, stream=None):
     """Gradients of sum(dy * y) + <dfinal, final_state> for the forward of the

@@ -42,9 +42,23 @@ def norm(dtype, K, V):
     return call
 
 
+def chunked(dtype, K, V):
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rnd = lambda *s, dt=dtype: torch.randn(s, generator=g, device="cuda").to(dt)  # noqa: E731
+    x, Bm, Cm, dy, D = rnd(2, 512, 4, V), rnd(2, 512, 1, K), rnd(2, 512, 1, K), rnd(2, 512, 4, V), rnd(4, dt=F32)
+    a = -torch.rand(2, 512, 4, generator=g, device="cuda")
+
+    def call(stream):
+        y, final = ssd.forward(x, a, Bm, Cm, D, 128, stream=stream)
+        return {"y": y, "final": final, **ssd.backward(x, a, Bm, Cm, D, dy, 128, dfinal=final, stream=stream)}
+
+    return call
+
+
 @pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
 @pytest.mark.parametrize("make,dtype,K,V", [(linear, BF, 128, 64), (linear, BF, 64, 64), (linear, F32, 24, 20),
-                                            (norm, BF, 1536, 64), (norm, F32, 700, 700)])
+                                            (norm, BF, 1536, 64), (norm, F32, 700, 700), (chunked, BF, 128, 64),
+                                            (chunked, F32, 24, 20)])
 def test_the_callers_stream_is_busy(make, dtype, K, V, handle):
     call = make(dtype, K, V)
     want = call(None)

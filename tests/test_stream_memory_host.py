@@ -121,6 +121,24 @@ CALLS = {
     "norm_backward": lambda s: ssd.layer_norm_backward(X, W, W, X, STATS, groups=2, stream=s),
 }
 
+XS, A, BM, D = t(2, 8, 4, 16), t(2, 8, 4, dtype=F32), t(2, 8, 1, 32), t(4, dtype=F32)
+STATE, SHAPE = t(2, 4, 32, 16, dtype=F32), ssd.make_shape(2, 8, 4, 16, 1, 32, 8)
+CALLS |= {
+    "forward": lambda s: ssd.forward(XS, A, BM, BM, D, 8, stream=s),
+    "forward_init": lambda s: ssd.forward(XS, A, BM, BM, D, 8, initial_state=STATE, stream=s),
+    "forward_noalloc": lambda s: ssd.forward_noalloc(XS, A, BM, BM, D, 8, stream=s),
+    "forward_discretized": lambda s: ssd.forward_discretized(XS, A, D, D, BM, BM, D, 8, stream=s),
+    "backward": lambda s: ssd.backward(XS, A, BM, BM, D, XS, 8, stream=s),
+    "decode_step": lambda s: ssd.decode_step(t(2, 4, 16), t(2, 4, dtype=F32), t(2, 1, 32), t(2, 1, 32), D, STATE, stream=s),
+    "discretize": lambda s: ssd.discretize(A, D, D, XS, stream=s),
+    "decay_total": lambda s: ssd.decay_total(A, stream=s),
+    "segment_state": lambda s: ssd.segment_state(XS, A, BM, 8, stream=s),
+    "state_combine": lambda s: ssd.state_combine(t(3, 2, 4, 32, 16, dtype=F32), t(3, 2, 4, dtype=F32), stream=s),
+    "chunk_cumsum": lambda s: ssd.chunk_cumsum(SHAPE, A, None, s),
+    "chunk_state": lambda s: ssd.chunk_state(SHAPE, XS, BM, A, stream=s),
+    "chunk_scan": lambda s: ssd.chunk_scan(SHAPE, XS, BM, BM, A, STATE, stream=s),
+}
+
 
 def results(out):
     return [r for r in (out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,))
@@ -148,6 +166,11 @@ def test_what_the_caller_gave_stays_the_callers(world):
     y = t(20, 4, 128)
     out, final = ssd.linear_attention(Q, K, V, DECAY, cu_seqlens=CU, y=y, stream=SIDE)
     assert out is y and y.used_by == () and final.used_by == (MAIN,)
+
+
+def test_addresses_instead_of_tensors(world):
+    assert ssd.chunk_cumsum(SHAPE, 1 << 20, 1 << 21, stream=SIDE) == 1 << 21
+    assert world == [("ssd_chunk_cumsum", 6000)]
 
 
 def test_a_stream_of_another_device_is_refused(world):
