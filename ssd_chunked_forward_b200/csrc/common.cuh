@@ -10,6 +10,16 @@ namespace ssd {
 // Device status word values (the first int32 of the workspace).
 enum : int { kDevOk = 0, kDevTimeout = 5 };
 
+// Lets `kernel` be launched with as much dynamic shared memory as a block can have
+// beside `fixed` bytes of its own.  The limit is one number per kernel and device for
+// the whole process, so it is the same number whatever a call needs: with each call's
+// own size, another thread's smaller one could come between setting and launching.
+template <typename... P>
+inline cudaError_t allow_smem(void (*kernel)(P...), int fixed) {
+    constexpr int block = 227 * 1024;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, block - fixed);
+}
+
 // Element loads/stores: every kernel computes in fp32.
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

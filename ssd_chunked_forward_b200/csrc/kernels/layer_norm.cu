@@ -623,7 +623,7 @@ cudaError_t launch(const NormArgs& a, NormShape& s, bool backward, cudaStream_t 
     auto kernel = backward ? (a.gate ? layer_norm_backward_kernel<T, VEC, NV, true> : layer_norm_backward_kernel<T, VEC, NV, false>)
                            : (a.gate ? layer_norm_kernel<T, VEC, NV, true> : layer_norm_kernel<T, VEC, NV, false>);
     if (smem > 40 * 1024) {  // (some KB are static)
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = allow_smem(kernel, 1024);
         if (e != cudaSuccess) return e;
     }
     if (s.most * s.slabs > 148) {

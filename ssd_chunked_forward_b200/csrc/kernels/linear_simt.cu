@@ -448,7 +448,7 @@ cudaError_t launch_scan_simt(const ScanLaunch& s, bool state_only, cudaStream_t 
     const size_t smem = simt_layout(K).bytes;
     auto kernel = s.bf16 ? (state_only ? scan_simt_kernel<__nv_bfloat16, false> : scan_simt_kernel<__nv_bfloat16, true>)
                          : (state_only ? scan_simt_kernel<float, false> : scan_simt_kernel<float, true>);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kernel, 1024);
     if (e != cudaSuccess) return e;
     return launch_in_call(kernel, (unsigned)grid, kThreads, smem, st, !s.reset, s, ntiles);
 }
