@@ -395,8 +395,7 @@ template <typename T, bool ANTI, bool VEC>
 cudaError_t launch_form_v(const Dims& d, Opd U, Opd V, Opd Z, const float* cum, const float* Mst,
                           int sk, int sm, float* out, int K, int Mc, cudaStream_t st) {
     const size_t smem = (size_t)(2 * K * kFS + 2 * kFT * kFS + 2 * kFT) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(chunk_form_kernel<T, ANTI, VEC>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(chunk_form_kernel<T, ANTI, VEC>, 0);
     if (e != cudaSuccess) return e;
     dim3 grid(d.nc * ((d.Q + kFT - 1) / kFT), d.B * d.H, (Mc + kFT - 1) / kFT);
     chunk_form_kernel<T, ANTI, VEC><<<grid, 256, smem, st>>>(U, V, Z, cum, Mst, sk, sm, out, d.T, d.H,

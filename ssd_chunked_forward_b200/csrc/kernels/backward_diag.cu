@@ -435,9 +435,7 @@ cudaError_t run_forms(const Dims& d, const BackwardArgs& g, const BackwardScratc
     cudaError_t e;
     {
         const size_t smem = (size_t)(4 * d.N * kFS + 2 * kFT * kFS + d.N) * sizeof(float);
-        if ((e = cudaFuncSetAttribute(dx_diag_kernel<T, VEC>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
-            return e;
+        if ((e = allow_smem(dx_diag_kernel<T, VEC>, 0))) return e;
         dim3 grid(d.nc * nrt, d.B * d.H, (d.P + kFT - 1) / kFT);
         dx_diag_kernel<T, VEC><<<grid, 256, smem, st>>>(oB, oC, ody, w.cum, w.dstates, w.dxt, d.T,
                                                         d.H, d.N, d.P, d.Q, d.nc);
@@ -446,16 +444,12 @@ cudaError_t run_forms(const Dims& d, const BackwardArgs& g, const BackwardScratc
     {
         const size_t smem = (size_t)(2 * d.P * kFS + 4 * kFT * kFS + kFT) * sizeof(float);
         dim3 grid(d.nc * nrt, d.B * d.H, (d.N + kFT - 1) / kFT);
-        if ((e = cudaFuncSetAttribute(dbc_diag_kernel<T, false, VEC>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
-            return e;
+        if ((e = allow_smem(dbc_diag_kernel<T, false, VEC>, 0))) return e;
         // dC: U = dy, V = x, Z = B, M = Hin^T
         dbc_diag_kernel<T, false, VEC><<<grid, 256, smem, st>>>(ody, ox, oB, w.cum, w.states, w.dCh,
                                                                 d.T, d.H, d.N, d.P, d.Q, d.nc);
         if ((e = cudaGetLastError())) return e;
-        if ((e = cudaFuncSetAttribute(dbc_diag_kernel<T, true, VEC>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
-            return e;
+        if ((e = allow_smem(dbc_diag_kernel<T, true, VEC>, 0))) return e;
         // dB: U = x, V = dy, Z = C, M = G^T
         dbc_diag_kernel<T, true, VEC><<<grid, 256, smem, st>>>(ox, ody, oC, w.cum, w.dstates, w.dBh,
                                                                d.T, d.H, d.N, d.P, d.Q, d.nc);

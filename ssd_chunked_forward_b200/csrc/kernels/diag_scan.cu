@@ -182,8 +182,7 @@ cudaError_t launch_diag_scan_simt(const Dims& d, const void* x, const void* Bm, 
         (size_t)(3 * 32 * NS + ((d.N + 3) & ~3) + 2 * d.N * 36 + 32 * 68 + 32 * 33 + 32 * 68) * sizeof(float);
 #define SSD_DIAG_LAUNCH(TT)                                                                        \
     do {                                                                                           \
-        e = cudaFuncSetAttribute(diag_scan_simt_kernel<TT>,                                        \
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dsmem);         \
+        e = allow_smem(diag_scan_simt_kernel<TT>, 0);                                              \
         if (e != cudaSuccess) return e;                                                            \
         diag_scan_simt_kernel<TT><<<grid, 256, dsmem, st>>>(                                       \
             (const TT*)x, (const TT*)Bm, (const TT*)Cm, cum, Hin, D, (TT*)y, d.T, d.H, d.P, d.G,   \

@@ -88,9 +88,7 @@ cudaError_t launch_chunk_cumsum(const Dims& d, const float* a, float* cum, cudaS
         dim3 grid(d.nc, d.B, (d.H + kCumHeads - 1) / kCumHeads);
         size_t smem = (size_t)d.Q * kCumHeads * sizeof(float);
         if (smem > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(chunk_cumsum_scalar_kernel,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem);
+            cudaError_t e = allow_smem(chunk_cumsum_scalar_kernel, 0);
             if (e != cudaSuccess) return e;
         }
         chunk_cumsum_scalar_kernel<<<grid, 256, smem, st>>>(a, cum, d.T, d.H, d.Q, d.nc);
@@ -414,8 +412,7 @@ cudaError_t launch_chunk_scan_simt(const Dims& d, const void* x, const void* Bm,
     smem += (size_t)64 * sizeof(float);
 #define SSD_SCAN_LAUNCH(TT)                                                                       \
     do {                                                                                          \
-        e = cudaFuncSetAttribute(chunk_scan_simt_kernel<TT>,                                      \
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);         \
+        e = allow_smem(chunk_scan_simt_kernel<TT>, 0);                                            \
         if (e != cudaSuccess) return e;                                                           \
         chunk_scan_simt_kernel<TT><<<grid, 256, smem, st>>>(                                      \
             (const TT*)x, (const TT*)Bm, (const TT*)Cm, cum, Hin, D, (TT*)y, d.T, d.H, d.P, d.G, \

@@ -41,32 +41,69 @@ def norm(dtype, width, backward):
     return call
 
 
+def chunked(dtype, P, N, backward, per_state=False):
+    """Kernels on CUDA cores, whose shared memory goes by the state's sizes."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    x, Bm, Cm = rnd(1, 8, 1, P), rnd(1, 8, 1, N), rnd(1, 8, 1, N)
+    a = -torch.rand((1, 8, 1, N) if per_state else (1, 8, 1), generator=g, device="cuda")
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    if not backward:
+        return lambda: ssd.forward(x, a, Bm, Cm, None, 8, path=ssd.PATH_SIMT, workspace=ws)
+
+    def call():
+        g = ssd.backward(x, a, Bm, Cm, None, x, 8, want_dD=False, workspace=ws)
+        return g["dx"], g["da"], g["dBm"], g["dCm"], g["dinit"]
+
+    return call
+
+
 PAIRS = {"scan": (lambda: scan(F32, 256, 16), lambda: scan(F32, 20, 16)),
          "scan bf16": (lambda: scan(BF, 250, 30), lambda: scan(BF, 36, 30)),
          # (blocks of 512 threads, and of 384 and 320)
          "norm": (lambda: norm(BF, 8192, False), lambda: norm(BF, 6000, False)),
-         "norm gradients": (lambda: norm(F32, 4096, True), lambda: norm(F32, 2400, True))}
+         "norm gradients": (lambda: norm(F32, 4096, True), lambda: norm(F32, 2400, True)),
+         "chunked": (lambda: chunked(F32, 16, 256, False), lambda: chunked(F32, 16, 20, False)),
+         "per state": (lambda: chunked(F32, 16, 256, False, True), lambda: chunked(F32, 16, 20, False, True)),
+         "chunked gradients": (lambda: chunked(F32, 64, 128, True), lambda: chunked(F32, 64, 64, True)),
+         "per state gradients": (lambda: chunked(F32, 64, 128, True, True), lambda: chunked(F32, 64, 64, True, True))}
+
+
+class Recorder:
+    """The library, and every call that is made of it."""
+
+    def __init__(self, lib):
+        self.lib, self.calls = lib, []
+
+    def __getattr__(self, name):
+        fn = getattr(self.lib, name)
+        if name.endswith("size"):
+            return fn
+
+        def call(*args):
+            self.calls.append((fn, args))
+            return fn(*args)
+
+        return call
 
 
 @pytest.mark.parametrize("pair", PAIRS)
 def test_threads_side_by_side(pair, monkeypatch):
     calls = [make() for make in PAIRS[pair]]  # (hold the inputs while the threads run)
-    queued, call = [], ssd._call
-    monkeypatch.setattr(ssd, "_call", lambda where, dev, fn, *a: (queued.append((fn, a)), call(where, dev, fn, *a)))
+    lib = Recorder(ssd.load())
+    monkeypatch.setattr(ssd, "load", lambda: lib)
     out = [c() for c in calls]
+    (one, a), (other, b) = lib.calls
     want = [[t.clone() for t in o] for o in out]
     torch.cuda.synchronize()
     start, codes = threading.Barrier(4), [set() for _ in range(4)]
 
     def run(i):
-        fn, args = queued[i % 2]
-        stream = streams[i].cuda_stream
+        fn, args = (one, a) if i % 2 else (other, b)
         start.wait()
         for _ in range(10000):
-            codes[i].add(fn(*args, stream))
+            codes[i].add(fn(*args))
 
-    # the two of a size write the same results
-    streams = [torch.cuda.Stream() for _ in range(4)]
     threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
     for t in threads:
         t.start()
