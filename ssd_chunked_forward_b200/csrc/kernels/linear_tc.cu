@@ -162,8 +162,10 @@ struct Layout {
 // A bounded wait in few instructions (each role's loop is executed once per chunk,
 // and all of them together have to stay in the instruction cache; a call would
 // spill the state that the warps hold in registers).  A try sleeps up to a
-// microsecond; the longest wait of a healthy run is some tens of them, and after
-// 2^20 tries (25 ms at the very least, a second as a rule) the wait has failed.
+// microsecond; a wait is for other warps of the block and its own copies, some tens of
+// tries at most, and after 2^20 (25 ms at the very least, a second as a rule) it has
+// failed.  What takes as long as it takes, the call's earlier kernels, the whole block
+// has waited for before its first such wait.
 __device__ __forceinline__ bool wait_here(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -364,6 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         const int n = nch == 0 || i == 0 ? kBlk : i == 1 ? (rev || nch == 1 ? at_end : kBlk) : (rev && nch > 1 ? kBlk : at_end);
         sDec[i] = decay_power(la, i == 1 || (i == 2 && nch == 1) ? n - 1 + off0 : n);
     }
+    // an item that starts from a slot starts when the combination is done, however long
+    // that takes: before any role's first wait, whose limits are for the block's own work
+    if (kOut && it.slot_prev >= 0) wait_for_earlier();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -700,7 +705,6 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         auto v_of = [&](int c) -> int { return kLaneV ? lr : c0 + c; };
 #pragma unroll
         for (int c = 0; c < CH; ++c) h[c] = 0.f;
-        if (kOut && !from_init) wait_for_earlier();
         if (kOut && holds && (it.seg > 0 || R.init)) {
             const float* src = from_init ? R.init + chain * K * V : p.s.states + it.slot_prev * K * V;
             const long long sk = from_init ? R.init_k : V, sv = from_init ? R.init_v : 1;
