@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(const ScanLaunch p,
     next_may_start();
     if (p.reset && blockIdx.x == 0 && threadIdx.x == 0) *p.status = kDevOk;
     if (threadIdx.x < 32) {
-        ScanItem it = scan_item(p.plan, blockIdx.x / ntiles);
+        ScanItem it = scan_item(p.plan, blockIdx.x / ntiles, !kOut);
         if (it.valid) scan_item_tokens(it, p.plan.seg_tokens, p.role[it.role].reverse);
         if (threadIdx.x == 0) sItem = it;
     }
@@ -308,46 +308,21 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(const ScanLaunch p,
 __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, int tiles) {
     __shared__ ScanItem sItem;
     next_may_start();
-    const int HR = p.plan.H * p.plan.nroles;
     const long long cr = blockIdx.x / tiles;  // chain and role
     if (threadIdx.x < 32) {
-        ScanItem f;
-        f.valid = 0;
-        if (!p.plan.packed) {
-            f = scan_item(p.plan, p.plan.nfull + cr * p.plan.nseg);
-        } else {
-            // the first item of sequence cr / HR, behind the items of those before it
-            const int seq = (int)(cr / HR), lane = threadIdx.x;
-            const int begin = min(max(p.plan.cu[seq], 0), p.plan.T);
-            if (min(p.plan.cu[seq + 1], p.plan.T) - begin > p.plan.seg_tokens) {
-                long long before = 0;
-                for (int base = 0; base < seq; base += 32) {
-                    const int s = base + lane;
-                    int n = 0;
-                    if (s < seq) {
-                        const int c0 = min(max(p.plan.cu[s], 0), p.plan.T);
-                        const int len = min(max(p.plan.cu[s + 1], c0), p.plan.T) - c0;
-                        n = max(1, (len + p.plan.seg_tokens - 1) / p.plan.seg_tokens);
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-                    before += n;
-                }
-                f = scan_item(p.plan, before * HR + cr % HR);
-            }
-        }
+        const ScanItem f = scan_item(p.plan, p.plan.packed ? cr : p.plan.nfull + cr * p.plan.nseg, true);
         if (threadIdx.x == 0) sItem = f;
     }
     __syncthreads();
     const ScanItem it = sItem;
-    if (!it.valid || it.nseg < 2) {
+    if (!it.valid || it.nseg < 2 || it.seg > 0) {  // (packed: not a first item's number)
         if (blockIdx.x == 0) wait_for_earlier();
         return;
     }
     const ScanRole& R = p.role[it.role];
     const int K = R.K, V = R.V;
     const float la = p.decay[it.head];
-    const long long step = p.plan.packed ? HR : 1;
+    const long long step = p.plan.packed ? (long long)p.plan.H * p.plan.nroles : 1;
     const long long chain = (long long)it.seq * p.plan.H + it.head;
     const float2 whole = decay_power(la, p.plan.seg_tokens);
     // the first item of a backward scan is the sequence's last, shorter piece,
@@ -369,16 +344,14 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, i
                 if (SSD_INB(at, (long long)p.plan.B * p.plan.H * KV)) h[u] = R.init[at] * R.init_scale;
             }
         }
-        const long long last = it.slot + (it.nseg - 1) * step;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int e = e0 + u * apart;
-            const long long at = last * KV + e;
-            if (R.init && e < KV && last < p.plan.slots() && SSD_INB(at, p.plan.slots() * KV)) p.states[at] = h[u];
+            const long long at = it.slot_init * KV + e;
+            if (R.init && e < KV && SSD_INB(at, p.plan.slots() * KV)) p.states[at] = h[u];
         }
         for (int i = 0; i + 1 < it.nseg; ++i) {
             const long long slot = it.slot + i * step;
-            if (slot >= p.plan.slots()) break;  // decreasing offsets: the items behind do not run
             const float2 d = i == 0 ? first : whole;
             float z[U];
 #pragma unroll
@@ -443,7 +416,7 @@ cudaError_t launch_scan_simt(const ScanLaunch& s, bool state_only, cudaStream_t 
         K = s.role[r].K > K ? s.role[r].K : K;
     }
     const int ntiles = (V + kVT - 1) / kVT;
-    const long long grid = s.plan.items * ntiles;
+    const long long grid = (state_only ? s.plan.state_items() : s.plan.items) * ntiles;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     const size_t smem = simt_layout(K).bytes;
     auto kernel = s.bf16 ? (state_only ? scan_simt_kernel<__nv_bfloat16, false> : scan_simt_kernel<__nv_bfloat16, true>)
@@ -456,10 +429,8 @@ cudaError_t launch_scan_simt(const ScanLaunch& s, bool state_only, cudaStream_t 
 cudaError_t launch_scan_combine(const ScanLaunch& s, cudaStream_t st) {
     int KV = 1;
     for (int r = 0; r < s.plan.nroles; ++r) KV = s.role[r].K * s.role[r].V > KV ? s.role[r].K * s.role[r].V : KV;
-    // enough blocks to fill the GPU, none more: with many packed sequences most
-    // blocks find an uncut chain and leave
-    const long long all = (long long)s.plan.B * s.plan.H * s.plan.nroles;
-    const long long chains = s.plan.packed ? all : all - s.plan.nfull;
+    // enough blocks to fill the GPU, none more
+    const long long chains = s.plan.cut_chains();
     int tiles = (KV + 1023) / 1024;  // (four elements a thread)
     while (tiles > 1 && chains * tiles > 148 * 8) tiles = (tiles + 1) / 2;
     const long long grid = chains * tiles;

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     next_may_start();
     if (p.s.reset && blockIdx.x == 0 && threadIdx.x == 0) *p.s.status = kDevOk;
     if (warp == 0) {
-        ScanItem f = scan_item(p.s.plan, blockIdx.x);
+        ScanItem f = scan_item(p.s.plan, blockIdx.x, !kOut);
         if (f.valid) scan_item_tokens(f, p.s.plan.seg_tokens, p.s.role[f.role].reverse);
         if (lane == 0) *sItem = f;
     }
@@ -945,11 +945,12 @@ cudaError_t role_maps(const ScanRole& r, const ScanPlan& p, CUtensorMap* m) {
 
 template <int KP, int VP, bool kOut, int kPieces>
 cudaError_t launch(const TcParams& p, cudaStream_t st) {
+    const long long grid = kOut ? p.s.plan.items : p.s.plan.state_items();
     auto kernel = scan_tc_kernel<KP, VP, kOut, kPieces>;
     constexpr size_t smem = Layout<KP, VP, kOut, kPieces>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_in_call(kernel, (unsigned)p.s.plan.items, kThreads, smem, st, !p.s.reset, p);
+    return launch_in_call(kernel, (unsigned)grid, kThreads, smem, st, !p.s.reset, p);
 }
 
 template <int KP, int VP>

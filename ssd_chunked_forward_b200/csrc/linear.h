@@ -53,10 +53,21 @@ constexpr int kScanChunk = 128;  // tokens of a chunk on tensor cores
 // How the chains (sequence, head, role) are cut into items, one per block.
 // Rows of equal length ([B][T]): the first `nfull` chains are one item each,
 // the others `nseg` items of seg_tokens tokens.  Packed rows: every sequence
-// is cut every seg_tokens tokens, and the items are counted on the device.
+// is cut every seg_tokens tokens, and the items are found on the device.
 // A chain of several items first has the state of each item but its last
 // built from zero (state-only items), then those states combined into the
 // state entering each item.
+//
+// Packed rows have their numbers from the offsets alone, so that a block finds its
+// item by a search in them and nothing has to be counted first.  With d = seg_tokens
+// and f(x) = floor(x / d), sequence s (rows a to b, all its heads and roles side by side)
+// owns the numbers
+//     s + f(a) ..    for its items: max(1, ceil((b-a) / d)) <= 1 + f(b) - f(a)
+//     f(a) ..        for its items but the last: ceil((b-a) / d) - 1 <= f(b) - f(a)
+// so the numbers of two sequences never meet, those of the second kind belong to
+// cut sequences alone, and there are at most B + f(T) and f(T) of them (some stand for
+// nothing).  The slots are numbered like the second kind; behind them, at
+// f(T) + f(a), lies the slot for the initial state of the chain's first item.
 struct ScanPlan {
     int B, T, H, nroles;
     int packed;
@@ -66,7 +77,12 @@ struct ScanPlan {
     long long items;    // upper bound when packed
     // whether any chain can have several items
     SSD_HD bool cut() const { return packed ? T > seg_tokens : nseg > 1; }
-    SSD_HD long long slots() const { return !cut() ? 0 : packed ? items : items - nfull; }
+    // packed: numbers of the second kind, over all heads and roles
+    SSD_HD long long inner() const { return (long long)(T / seg_tokens) * H * nroles; }
+    SSD_HD long long slots() const { return !cut() ? 0 : packed ? 2 * inner() : items - nfull; }
+    // blocks of a state-only launch, and chains whose states are combined
+    SSD_HD long long state_items() const { return packed ? inner() : items; }
+    SSD_HD long long cut_chains() const { return packed ? inner() : (long long)B * H * nroles - nfull; }
 };
 
 struct ScanLaunch {
@@ -87,34 +103,96 @@ struct ScanItem {
     int batch;              // batch coordinate (0 when packed)
     int len;                // tokens of the sequence
     int t0, t1;             // this item's tokens [t0, t1) of the sequence
-    // states: own, and the one this item starts from.  A cut chain's first item starts
-    // from its last one's slot, where the initial state is put (it may be read late, when
-    // the final state, which may be the same memory, is written); -1: not cut
-    long long slot, slot_prev;
+    // states: own (of an item that is not its chain's last), the one this item starts from,
+    // and the chain's slot for the initial state, where its first item finds it (it may be read
+    // late, when the final state, which may be the same memory, is written).  -1: not cut
+    long long slot, slot_prev, slot_init;
     int valid;
 };
 
+// The first number of packed sequence s, whose rows start at a.
+SSD_HD inline unsigned packed_first(const ScanPlan& p, int s, int a, bool inner) {
+    return (inner ? 0u : (unsigned)s) + (unsigned)a / (unsigned)p.seg_tokens;
+}
+// Number `number`, place hr among the heads and roles, as an item of packed sequence s
+// (rows a to b).
+SSD_HD inline void packed_item(const ScanPlan& p, unsigned number, int hr, int s, int a, int b, bool inner,
+                               ScanItem& r) {
+    const int HR = p.H * p.nroles, first = a / p.seg_tokens;
+    r.seq = s;
+    r.row0 = a;
+    r.batch = 0;
+    r.len = b - a;
+    r.head = hr / p.nroles;
+    r.role = hr - r.head * p.nroles;
+    r.nseg = r.len <= p.seg_tokens ? 1 : (r.len - 1) / p.seg_tokens + 1;
+    r.seg = (int)(number - packed_first(p, s, a, inner));
+    r.valid = r.seg < r.nseg;  // else a number that stands for nothing
+    if (!r.valid || r.nseg == 1) return;
+    r.slot = (long long)(first + r.seg) * HR + hr;
+    r.slot_init = ((long long)(p.T / p.seg_tokens) + first) * HR + hr;
+    r.slot_prev = r.seg > 0 ? r.slot - HR : r.slot_init;
+}
+
+// The tokens of the item, given the direction of its role.
+SSD_HD inline void scan_item_tokens(ScanItem& r, int seg_tokens, int reverse) {
+    if (r.nseg == 1) {
+        r.t0 = 0;
+        r.t1 = r.len;
+    } else {
+        const int j = reverse ? r.nseg - 1 - r.seg : r.seg;
+        r.t0 = j * seg_tokens;
+        r.t1 = r.t0 + seg_tokens < r.len ? r.t0 + seg_tokens : r.len;
+    }
+}
+
 #ifdef __CUDACC__
-// Called by the 32 lanes of one warp; the result is the same in every lane.
-// Offsets that are no offsets (negative, beyond T, decreasing) are clamped, so
-// that no row outside [0, T) is ever addressed.
-__device__ inline ScanItem scan_item(const ScanPlan& p, long long it) {
+// The last of the B packed sequences whose first number is at most `number`, and
+// its offsets a and b; -1 if there is none.  Called by the 32 lanes of one warp, which
+// look at 32 places at a time: B sequences take log33 B rounds.  Offsets that are no
+// offsets (negative, beyond T, decreasing) are clamped, so that no row outside [0, T)
+// and no slot outside the workspace is ever addressed.
+__device__ inline int packed_sequence(const ScanPlan& p, unsigned number, bool inner, int& a, int& b) {
+    const int lane = threadIdx.x & 31;
+    auto offset = [&](int s) { return min(max(p.cu[s], 0), p.T); };
+    int lo = -1, hi = p.B, at_lo = 0, at_hi = offset(p.B);
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 32) / 33;
+        const long long place = lo + (lane + 1LL) * step;
+        const bool there = place < hi;
+        const int s = there ? (int)place : hi;
+        const int c = there ? offset(s) : at_hi;
+        const unsigned below = __ballot_sync(0xffffffffu, there && packed_first(p, s, c, inner) <= number);
+        const int n = below == 0xffffffffu ? 32 : __ffs(~below) - 1;  // places in front that are
+        const int next = __shfl_sync(0xffffffffu, s, n & 31), at_next = __shfl_sync(0xffffffffu, c, n & 31);
+        const int last = __shfl_sync(0xffffffffu, s, (n + 31) & 31), at_last = __shfl_sync(0xffffffffu, c, (n + 31) & 31);
+        if (n < 32) hi = next, at_hi = at_next;
+        if (n > 0) lo = last, at_lo = at_last;
+    }
+    a = at_lo;
+    b = max(at_hi, at_lo);
+    return lo;
+}
+// Item `it` of a plan: of the main launch's, or (inner) of the state-only launch's,
+// which for packed rows has numbers of the second kind.  Called by the 32 lanes of one
+// warp; the result is the same in every lane.
+__device__ inline ScanItem scan_item(const ScanPlan& p, long long it, bool inner) {
     ScanItem r;
     r.valid = 0;
     r.row0 = 0;
-    // an item is a block of a grid: 32 bits hold it, and their divisions are short.
-    // (Packed offsets that decrease can ask for more items than there are slots for.)
-    if (it >= p.items) return r;
+    r.slot = r.slot_prev = r.slot_init = -1;
     if (!p.packed) {
+        // an item is a block of a grid: 32 bits hold it, and their divisions are short
         unsigned cr = (unsigned)it;
         int seg = 0, nseg = 1;
-        r.slot = -1;
         if (it >= p.nfull) {
             const unsigned rest = cr - (unsigned)p.nfull, chain = rest / (unsigned)p.nseg;
             cr = (unsigned)p.nfull + chain;
             seg = (int)(rest - chain * (unsigned)p.nseg);
             nseg = p.nseg;
             r.slot = rest;
+            r.slot_init = r.slot - seg + nseg - 1;
+            r.slot_prev = seg > 0 ? r.slot - 1 : nseg > 1 ? r.slot_init : -1;
         }
         const unsigned hr = p.nroles == 1 ? cr : cr / (unsigned)p.nroles;
         r.role = (int)(cr - hr * (unsigned)p.nroles);
@@ -124,63 +202,14 @@ __device__ inline ScanItem scan_item(const ScanPlan& p, long long it) {
         r.len = p.T;
         r.seg = seg;
         r.nseg = nseg;
-        r.slot_prev = seg > 0 ? r.slot - 1 : nseg > 1 ? r.slot + nseg - 1 : -1;
         r.valid = 1;
     } else {
-        const int lane = threadIdx.x & 31;
-        const int HR = p.H * p.nroles;
-        const long long unit = (unsigned)it / (unsigned)HR;
-        const int hr = (int)((unsigned)it - (unsigned)unit * (unsigned)HR);
-        r.head = hr / p.nroles;
-        r.role = hr - r.head * p.nroles;
-        r.batch = 0;
-        long long before = 0;
-        int found = 0;
-        for (int base = 0; base < p.B && !found; base += 32) {
-            const int s = base + lane;
-            int c0 = 0, len = 0, n = 0;
-            if (s < p.B) {
-                c0 = min(max(p.cu[s], 0), p.T);
-                len = min(max(p.cu[s + 1], c0), p.T) - c0;
-                n = max(1, (len + p.seg_tokens - 1) / p.seg_tokens);
-            }
-            int sum = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += u;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, before + sum > unit);
-            if (hit) {
-                const int w = __ffs(hit) - 1;
-                r.seq = base + w;
-                r.row0 = __shfl_sync(0xffffffffu, c0, w);
-                r.len = __shfl_sync(0xffffffffu, len, w);
-                r.nseg = __shfl_sync(0xffffffffu, n, w);
-                r.seg = (int)(unit - before) - (__shfl_sync(0xffffffffu, sum, w) - r.nseg);
-                found = 1;
-            } else {
-                before += __shfl_sync(0xffffffffu, sum, 31);
-            }
-        }
-        if (!found) return r;
-        r.slot = it;
-        r.slot_prev = r.seg > 0 ? it - HR : r.nseg > 1 ? it + (long long)(r.nseg - 1) * HR : -1;
-        if (r.slot_prev >= p.items) return r;
-        r.valid = 1;
+        const unsigned HR = (unsigned)(p.H * p.nroles), number = (unsigned)it / HR;
+        int a, b;
+        const int seq = packed_sequence(p, number, inner, a, b);
+        if (seq >= 0) packed_item(p, number, (int)((unsigned)it - number * HR), seq, a, b, inner, r);
     }
     return r;
-}
-// The tokens of the item, given the direction of its role.
-__device__ inline void scan_item_tokens(ScanItem& r, int seg_tokens, int reverse) {
-    if (r.nseg == 1) {
-        r.t0 = 0;
-        r.t1 = r.len;
-    } else {
-        const int j = reverse ? r.nseg - 1 - r.seg : r.seg;
-        r.t0 = j * seg_tokens;
-        r.t1 = min(r.len, r.t0 + seg_tokens);
-    }
 }
 // exp(decay * n) as an unevaluated sum of two fp32 numbers: a long chain
 // multiplies its state by the same factor at every chunk, and the error of one
