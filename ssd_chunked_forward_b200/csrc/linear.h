@@ -142,7 +142,7 @@ SSD_HD inline void scan_item_tokens(ScanItem& r, int seg_tokens, int reverse) {
     } else {
         const int j = reverse ? r.nseg - 1 - r.seg : r.seg;
         r.t0 = j * seg_tokens;
-        r.t1 = r.t0 + seg_tokens < r.len ? r.t0 + seg_tokens : r.len;
+        r.t1 = r.len - r.t0 > seg_tokens ? r.t0 + seg_tokens : r.len;  // (len may be near 2^31)
     }
 }
 

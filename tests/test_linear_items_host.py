@@ -100,7 +100,31 @@ static void run(const std::vector<int>& cu, int T, int seg, int H, int roles, bo
     if (p.cut()) NEED(most <= 2LL * (T / seg) * HR);
 }
 
+// the last item of a sequence whose length is the largest that a call takes
+static void longest(int seg, int packed) {
+    ScanPlan p = {};
+    p.B = 1; p.T = 0x7fffffff - 1024; p.H = p.nroles = 1; p.packed = packed; p.seg_tokens = seg;
+    const int n = (p.T - 1) / seg + 1;
+    long long tokens = 0;
+    for (int i = 0; i < n; ++i) {
+        ScanItem r; r.slot = r.slot_prev = r.slot_init = -1;
+        if (packed) packed_item(p, (unsigned)i, 0, 0, 0, p.T, false, r);
+        else r.len = p.T, r.seg = i, r.nseg = n;
+        NEED(r.nseg == n);
+        scan_item_tokens(r, seg, i & 1);
+        NEED(r.t0 >= 0 && r.t0 < r.t1 && r.t1 <= p.T);
+        scan_item_tokens(r, seg, 0);
+        tokens += r.t1 - r.t0;
+    }
+    NEED(tokens == p.T);
+}
+
 int main() {
+    for (int packed = 0; packed < 2; ++packed) {
+        longest(1 << 30, packed);
+        longest(4836224, packed);
+        longest(512, packed);
+    }
     std::srand(7);
     for (int round = 0; round < 4000; ++round) {
         const int B = 1 + std::rand() % 40, T = 1 + std::rand() % 3000, seg = 1 + std::rand() % 400;
