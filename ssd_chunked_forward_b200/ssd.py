@@ -603,6 +603,16 @@ def _on_device(name, t, device, dtype=None, shape=None, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _on_boundary(name, t, by):
+    if t.data_ptr() % by:
+        raise ValueError(f"{name} must start on a {by}-byte boundary")
+
+
+def _aligned(t):
+    """A tensor that is only read, on a 16-byte boundary: itself or a copy."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _dtype_code(dtype):
     if dtype == torch.bfloat16:
         return SSD_DTYPE_BF16
@@ -695,6 +705,7 @@ def _workspace_arg(workspace, need, device):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
     _on_device("workspace", workspace, device, torch.uint8)
+    _on_boundary("workspace", workspace, 256)
     return workspace
 
 
@@ -718,7 +729,8 @@ def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqle
     or None (zero), scale (None: K**-0.5).  With cu_seqlens (int32 [S+1], on the device) the
     tensors are [T,heads,d] with S sequences one behind the other, the states
     [S,H,K,V]; rows of a given y outside every sequence stay as they are (those
-    of a new y are not set).
+    of a new y are not set).  A given y and final_state (which may be initial_state)
+    start on 16-byte boundaries, other states are taken from anywhere.
     Returns y [B,T,H,V] and the state [B,H,K,V] float32 (None with
     want_final=False).  Asynchronous on the current stream of q's device."""
     plan, dev = _linear_plan(q, k, v, decay, cu_seqlens), q.device
@@ -728,11 +740,14 @@ def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqle
         y = torch.empty(plan.y, dtype=q.dtype, device=dev)
     else:
         _on_device("y", y, dev, q.dtype, plan.y)
+        _on_boundary("y", y, 16)
     if final_state is not None:
         _on_device("final_state", final_state, dev, torch.float32, plan.state)
+        _on_boundary("final_state", final_state, 16)
     elif want_final:
         final_state = torch.empty(plan.state, dtype=torch.float32, device=dev)
     workspace = _workspace_arg(workspace, plan.forward_bytes, dev)
+    initial_state = _aligned(initial_state)
     shape, sq, sk, sv = plan.refs
     _call("ssd_linear_attention", dev, load().ssd_linear_attention, shape, q.data_ptr(), sq, k.data_ptr(), sk,
           v.data_ptr(), sv, decay.data_ptr(), _ptr(cu_seqlens), _ptr(initial_state),
@@ -744,10 +759,12 @@ def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqle
 @_on_its_stream
 def linear_attention_step(q, k, v, decay, state, *, scale=None, y=None, stream=None):
     """One token of linear_attention() for a batch of sequences, in place on
-    ``state`` [B,H,K,V] float32: q [B,H,K], k [B,G,K], v [B,G,V], decay [H].
+    ``state`` [B,H,K,V] float32, on a 16-byte boundary: q [B,H,K], k [B,G,K],
+    v [B,G,V], decay [H].
     Returns y [B,H,V]."""
     plan, dev = _linear_plan(q, k, v, decay, None, True), q.device
     _on_device("state", state, dev, torch.float32, plan.state)
+    _on_boundary("state", state, 16)
     if y is None:
         y = torch.empty(plan.y, dtype=q.dtype, device=dev)
     else:
@@ -776,6 +793,7 @@ def linear_attention_backward(q, k, v, decay, dy, *, scale=None, initial_state=N
     dq, dk, dv = (new(d, dtype=q.dtype, device=dev) for d in (q.shape, plan.k, plan.v))
     dinit = torch.empty(plan.state, dtype=torch.float32, device=dev) if want_dinit else None
     workspace = _workspace_arg(workspace, plan.backward_bytes, dev)
+    dy, initial_state, dfinal = _aligned(dy), _aligned(initial_state), _aligned(dfinal)
     shape, sq, sk, sv = plan.refs
     _call("ssd_linear_attention_backward", dev, load().ssd_linear_attention_backward, shape, q.data_ptr(), sq,
           k.data_ptr(), sk, v.data_ptr(), sv, decay.data_ptr(), _ptr(cu_seqlens), _ptr(initial_state),
@@ -871,6 +889,7 @@ def layer_norm_backward(x, weight, bias, dy, stats, *, groups=1, gate=None, want
     float32, or None)."""
     plan, dev = _norm_plan(x, weight, bias, groups, gate, dy), x.device
     _on_device("stats", stats, dev, torch.float32, plan.stats)
+    _on_boundary("stats", stats, 8)
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
     dgate = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
     dweight = torch.empty(plan.width, dtype=torch.float32, device=dev) if want_dweight else None
