@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(const ScanLaunch p,
     next_may_start();
     if (p.reset && blockIdx.x == 0 && threadIdx.x == 0) *p.status = kDevOk;
     if (threadIdx.x < 32) {
-        ScanItem it = scan_item(p.plan, blockIdx.x / ntiles, !kOut);
+        ScanItem it = scan_item(p.plan, blockIdx.x / ntiles);
         if (it.valid) scan_item_tokens(it, p.plan.seg_tokens, p.role[it.role].reverse);
         if (threadIdx.x == 0) sItem = it;
     }
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, i
     next_may_start();
     const long long cr = blockIdx.x / tiles;  // chain and role
     if (threadIdx.x < 32) {
-        const ScanItem f = scan_item(p.plan, p.plan.packed ? cr : p.plan.nfull + cr * p.plan.nseg, true);
+        const ScanItem f = scan_item(p.plan, p.plan.packed ? cr : p.plan.nfull + cr * p.plan.nseg);
         if (threadIdx.x == 0) sItem = f;
     }
     __syncthreads();
@@ -350,21 +350,24 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(const ScanLaunch p, i
             const long long at = it.slot_init * KV + e;
             if (R.init && e < KV && SSD_INB(at, p.plan.slots() * KV)) p.states[at] = h[u];
         }
-        for (int i = 0; i + 1 < it.nseg; ++i) {
-            const long long slot = it.slot + i * step;
+        // a slot's numbers are on their way while the one before is worked on
+        float* at = p.states + it.slot * KV + e0;
+        const long long next = step * KV;
+        float z[U];
+        auto fetch = [&](const float* from) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                z[u] = e0 + u * apart < KV && SSD_INB(from - p.states + u * apart, p.plan.slots() * KV) ? from[u * apart] : 0.f;
+        };
+        fetch(at);
+        for (int i = 0; i + 1 < it.nseg; ++i, at += next) {
             const float2 d = i == 0 ? first : whole;
-            float z[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const long long at = slot * KV + e0 + u * apart;
-                z[u] = e0 + u * apart < KV && SSD_INB(at, p.plan.slots() * KV) ? p.states[at] : 0.f;
-            }
+            for (int u = 0; u < U; ++u) h[u] = fmaf(h[u], d.x, fmaf(h[u], d.y, z[u]));
+            if (i + 2 < it.nseg) fetch(at + next);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const long long at = slot * KV + e0 + u * apart;
-                h[u] = fmaf(h[u], d.x, fmaf(h[u], d.y, z[u]));
-                if (e0 + u * apart < KV && SSD_INB(at, p.plan.slots() * KV)) p.states[at] = h[u];
-            }
+            for (int u = 0; u < U; ++u)
+                if (e0 + u * apart < KV && SSD_INB(at - p.states + u * apart, p.plan.slots() * KV)) at[u * apart] = h[u];
         }
     }
 }

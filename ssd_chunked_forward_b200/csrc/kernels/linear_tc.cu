@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     next_may_start();
     if (p.s.reset && blockIdx.x == 0 && threadIdx.x == 0) *p.s.status = kDevOk;
     if (warp == 0) {
-        ScanItem f = scan_item(p.s.plan, blockIdx.x, !kOut);
+        ScanItem f = scan_item(p.s.plan, blockIdx.x);
         if (f.valid) scan_item_tokens(f, p.s.plan.seg_tokens, p.s.role[f.role].reverse);
         if (lane == 0) *sItem = f;
     }

@@ -34,26 +34,24 @@ static void run(const std::vector<int>& cu, int T, int seg, int H, int roles, bo
     p.items = ((long long)p.B + T / seg) * H * roles;
     const int HR = H * roles;
     std::set<long long> slots;
+    const unsigned whole = T / seg;
     // what the warps' search finds: the last sequence whose first number is at most this one
-    // (offsets that decrease: some such sequence)
-    auto find = [&](unsigned number, bool inner, int& a, int& b) {
-        int s = -1;
-        for (int i = 0; i < p.B; ++i)
-            if (packed_first(p, i, clamp(cu[i], T), inner) <= number) s = i;
-        if (s >= 0) { a = clamp(cu[s], T); b = clamp(cu[s + 1], T); if (b < a) b = a; }
-        return s;
-    };
-    auto item = [&](long long it, bool inner) {
+    auto rows = [&](int s, int& a, int& b) { a = clamp(cu[s], T); b = std::max(a, clamp(cu[s + 1], T)); };
+    auto item = [&](long long it) {
         ScanItem r; r.valid = 0; r.slot = r.slot_prev = r.slot_init = -1;
-        int a = 0, b = 0;
-        const int s = find((unsigned)(it / HR), inner, a, b);
-        if (s >= 0) packed_item(p, (unsigned)(it / HR), (int)(it % HR), s, a, b, inner, r);
+        const unsigned number = (unsigned)(it / HR);
+        int a = 0, b = 0, s = -1;
+        if (number < whole) {
+            for (int i = 0; i < p.B; ++i)
+                if ((unsigned)clamp(cu[i], T) / seg <= number) s = i;
+        } else s = (int)(number - whole);
+        if (s >= 0) { rows(s, a, b); packed_item(p, number, (int)(it % HR), s, a, b, r); }
         return r;
     };
     std::vector<std::set<long long>> seen(p.B), states(p.B);
     long long most = p.slots();
     for (long long it = 0; it < p.items; ++it) {
-        ScanItem r = item(it, false);
+        ScanItem r = item(it);
         if (!r.valid) continue;
         for (int rev = 0; rev < 2; ++rev) {
             scan_item_tokens(r, seg, rev);
@@ -68,7 +66,7 @@ static void run(const std::vector<int>& cu, int T, int seg, int H, int roles, bo
         NEED(seen[r.seq].insert((long long)r.seg * HR + r.head * roles + r.role).second);
     }
     for (long long it = 0; p.cut() && it < p.state_items(); ++it) {
-        ScanItem r = item(it, true);
+        ScanItem r = item(it);
         if (!r.valid || r.seg == r.nseg - 1) continue;
         NEED(r.slot >= 0 && r.slot < most && r.slot_init < most);
         if (!valid) continue;
@@ -78,18 +76,19 @@ static void run(const std::vector<int>& cu, int T, int seg, int H, int roles, bo
     }
     if (!valid) {  // whichever sequence a search finds
         for (long long it = 0; it < p.items; ++it)
-            for (int s = 0; s < p.B; ++s)
-                for (int inner = 0; inner < (p.cut() && it < p.state_items() ? 2 : 1); ++inner) {
-                    const int a = clamp(cu[s], T), b = std::max(a, clamp(cu[s + 1], T));
-                    if (packed_first(p, s, a, inner) > (unsigned)(it / HR)) continue;
-                    ScanItem r; r.slot = r.slot_prev = r.slot_init = -1;
-                    packed_item(p, (unsigned)(it / HR), (int)(it % HR), s, a, b, inner, r);
-                    if (!r.valid) continue;
-                    scan_item_tokens(r, seg, 0);
-                    NEED(r.seg >= 0 && r.t0 >= 0 && r.t1 <= r.len && r.row0 + r.len <= T);
-                    if (r.nseg > 1) NEED(r.slot_prev >= 0 && r.slot_prev < most && r.slot_init < most);
-                    if (inner && r.seg < r.nseg - 1) NEED(r.slot >= 0 && r.slot < most);
-                }
+            for (int s = 0; s < p.B; ++s) {
+                const unsigned number = (unsigned)(it / HR);
+                int a, b;
+                rows(s, a, b);
+                if (number < whole ? (unsigned)a / seg > number : (int)(number - whole) != s) continue;
+                ScanItem r; r.slot = r.slot_prev = r.slot_init = -1;
+                packed_item(p, number, (int)(it % HR), s, a, b, r);
+                if (!r.valid) continue;
+                scan_item_tokens(r, seg, 0);
+                NEED(r.seg >= 0 && r.t0 >= 0 && r.t1 <= r.len && r.row0 + r.len <= T);
+                if (r.nseg > 1) NEED(r.slot_prev >= 0 && r.slot_prev < most && r.slot_init < most);
+                if (it < p.state_items() && r.seg < r.nseg - 1) NEED(r.slot >= 0 && r.slot < most);
+            }
         return;
     }
     for (int s = 0; s < p.B; ++s) {
@@ -108,7 +107,7 @@ static void longest(int seg, int packed) {
     long long tokens = 0;
     for (int i = 0; i < n; ++i) {
         ScanItem r; r.slot = r.slot_prev = r.slot_init = -1;
-        if (packed) packed_item(p, (unsigned)i, 0, 0, 0, p.T, false, r);
+        if (packed) packed_item(p, (unsigned)i, 0, 0, 0, p.T, r);
         else r.len = p.T, r.seg = i, r.nseg = n;
         NEED(r.nseg == n);
         scan_item_tokens(r, seg, i & 1);
