@@ -17,7 +17,7 @@
 // the call, so w o K must not lose bits: it (or w o V, whichever is 64 wide)
 // enters the product as kPieces bf16 numbers, the first ones its leading bits,
 // the last one rounded: 3 hold the fp32 product whole and are used where the
-// state is a result, 2 (error below 2^-17) where it only enters outputs.
+// state is a result, 2 (error up to 2^-16) where it only enters outputs.
 // l^n multiplies H at every chunk and is kept as a sum of two fp32 numbers, or
 // its rounding would grow with the number of chunks.
 //
