@@ -23,21 +23,9 @@
 namespace ssd {
 namespace {
 
-constexpr int kC = 32;        // tokens of a chunk
-constexpr int kVT = 64;       // state columns of a block
+constexpr int kC = kSimtChunk;     // tokens of a chunk
+constexpr int kVT = kSimtColumns;  // state columns of a block
 constexpr int kThreads = 256;
-
-struct SimtLayout {
-    int K4, ldk;  // K rounded up to 4, row pitch of q and k
-    size_t bytes;
-};
-__host__ __device__ inline SimtLayout simt_layout(int K) {
-    SimtLayout l;
-    l.K4 = (K + 3) & ~3;
-    l.ldk = l.K4 + 4;  // rows start 4 banks apart: eight rows' 16-byte reads meet no bank twice
-    l.bytes = (size_t)(2 * kC * l.ldk + kC * kVT + kC * (kC + 4) + l.K4 * kVT + kC + 4) * sizeof(float);
-    return l;
-}
 
 // rows [t, t+n) of a tensor, D of its columns from c0 on, into fp32 rows of
 // pitch ld; the rows behind n and the columns behind D up to Dp are zero

@@ -49,6 +49,23 @@ struct ScanRole {
 
 constexpr int kScanRoles = 3;
 constexpr int kScanChunk = 128;  // tokens of a chunk on tensor cores
+constexpr int kSimtChunk = 32;   // and on CUDA cores,
+constexpr int kSimtColumns = 64; // state columns of a block there
+
+// Shared memory of a block on CUDA cores: q and k rows, v, scores, state, powers.
+struct SimtLayout {
+    int K4, ldk;  // K rounded up to 4, row pitch of q and k
+    size_t bytes;
+};
+SSD_HD inline SimtLayout simt_layout(int K) {
+    SimtLayout l;
+    l.K4 = (K + 3) & ~3;
+    // an odd number of 16-byte units, so that eight rows' 16-byte reads meet no bank twice
+    l.ldk = l.K4 + (l.K4 % 8 == 0 ? 4 : 8);
+    l.bytes = (size_t)(2 * kSimtChunk * l.ldk + kSimtChunk * kSimtColumns + kSimtChunk * (kSimtChunk + 4) +
+                       l.K4 * kSimtColumns + kSimtChunk + 4) * sizeof(float);
+    return l;
+}
 
 // How the chains (sequence, head, role) are cut into items, one per block.
 // Rows of equal length ([B][T]): the first `nfull` chains are one item each,

@@ -92,15 +92,14 @@ ScanPlan make_plan(const ssd_linear_shape& s, int nroles, int vmax, bool tc, con
     p.H = s.H;
     p.nroles = nroles;
     // tensor cores: one block per SM; CUDA cores: two, of 64 state columns each
-    const int tiles = cdiv(vmax, 64);
+    const int tiles = cdiv(vmax, ssd::kSimtColumns);
     int at_once = tc ? kSMs : 2 * kSMs / tiles;
     // (CUDA cores: bounds every 128 tokens instead of 32 cost 52 against 33 us for 2 x 333
     // tokens of 8 heads; without the states' size in an item's start the gradients of 1 x 300
     // tokens, 24 heads, 128 x 128 took 173 us instead of 131)
-    constexpr int kSimtChunk = 32;
-    if (s.packed) plan_packed(p, at_once, tc ? ssd::kScanChunk : kSimtChunk, cu);
+    if (s.packed) plan_packed(p, at_once, tc ? ssd::kScanChunk : ssd::kSimtChunk, cu);
     else if (tc) plan_rows(p, at_once, ssd::kScanChunk, 1.5, 3.0);
-    else plan_rows(p, at_once, kSimtChunk, 0.5 * s.K * s.V / 4096.0, 1.0);
+    else plan_rows(p, at_once, ssd::kSimtChunk, 0.5 * s.K * s.V / 4096.0, 1.0);
     return p;
 }
 

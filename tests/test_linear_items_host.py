@@ -1,5 +1,5 @@
-"""How packed sequences are cut into items, from the header that the kernels use,
-compiled for the host: every token of every sequence is in one item, numbers and
+"""What the linear-attention kernels share, from their header, compiled for the host.
+How packed sequences are cut into items: every token of every sequence is in one item, numbers and
 slots never meet, and all of them lie inside the grid and the workspace, also for
 offsets that break the rules."""
 from __future__ import annotations
@@ -118,7 +118,21 @@ static void longest(int seg, int packed) {
     NEED(tokens == p.T);
 }
 
+// blocks on CUDA cores: eight neighbouring rows' 16-byte reads meet 32 different banks,
+// and every size fits
+static void layouts() {
+    for (int K = 1; K <= 256; ++K) {
+        const SimtLayout l = simt_layout(K);
+        std::set<int> banks;
+        for (int row = 0; row < 8; ++row)
+            for (int word = 0; word < 4; ++word) banks.insert((row * l.ldk + word) % 32);
+        NEED(banks.size() == 32 && l.ldk >= l.K4 && l.K4 >= K && l.ldk % 4 == 0);
+        NEED(l.bytes <= simt_layout(256).bytes && l.bytes <= 226 * 1024);
+    }
+}
+
 int main() {
+    layouts();
     for (int packed = 0; packed < 2; ++packed) {
         longest(1 << 30, packed);
         longest(4836224, packed);
@@ -146,7 +160,7 @@ int main() {
 """
 
 
-def test_items_of_packed_sequences(tmp_path):
+def test_items_and_layouts(tmp_path):
     src, exe = tmp_path / "items.cpp", tmp_path / "items"
     src.write_text(PROGRAM)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
