@@ -546,18 +546,23 @@ int norm_parts(const NormShape& s, int resident) {
 // numbers (sums, barriers, counting) is shared by all of them, so a thread takes two
 // vectors of a part (32768 x 2560: forward 71 us, with one 89; backward 104, with one
 // 137; 20000 x 2560 in 32 groups: 54 and 69, backward 78 and 102).  Exceptions:
-//   the gated backward of narrow parts, whose three tensors then spill registers
-//     (16384 x 1536 in 24 groups: 54 us with one, 59 with two; but 32768 x 5120
-//     in 80: 326 and 303);
-//   the plain forward of bf16 parts of more than 384 vectors takes four (16384 x 8192: 95 us,
-//     126 with two; gated 229 with four, 178 with two);
+//   the gated backward of narrow parts in vectors of eight, whose three tensors then
+//     spill registers.  Two against one vector, time: 1.27 at 16384 x 2048 in 64 groups,
+//     1.10 at 16384 x 1536 in 24 (58.4 us with one), 1.12 at 4096 x 5120 in 80, 1.09 at
+//     32768 x 2048 in 16; even at 65536 x 640 in 8; 0.97 to 0.99 from 80 million numbers on
+//     (32768 x 5120 in 80: 302 and 312 us).  Vectors of four do not spill: bf16
+//     0.76 at 65536 x 800 in 8 and 0.70 at 20000 x 1440 in 40, fp32 0.80 at 65536 x 640 in
+//     8, 0.96 at 32768 x 2560 in 80, 1.03 at most (8192 x 1536 in 24);
+//   the plain forward of bf16 parts of more than 384 vectors takes four.  Four against
+//     two: 0.76 at 16384 x 8192 (98 us), 0.78 at x 6144, 0.97 at x 5120, 0.94 at x 3200, 0.91
+//     at 32768 x 4096; 1.06 at 4096 x 4096.  (Gated 229 us with four, 178 with two);
 //   what the block could not hold otherwise.
 // A part of up to 32 threads is a team of lanes, and a block takes the parts and rows
 // that leave an SM's threads busiest; wider parts take a block each.
 void norm_shape(long long rows, int width, int groups, int vec, bool gate, bool backward, NormShape* s, int* nv) {
     s->n = width / groups;
     const int v = (s->n + vec - 1) / vec;
-    *nv = vec > 2 && v >= 4 && (v > 32 || !(backward && gate)) ? 2 : 1;
+    *nv = vec > 2 && v >= 4 && (v > 32 || vec < 8 || !(backward && gate)) ? 2 : 1;
     // threads that an SM holds at the kernels' registers
     const int hold = *nv == 1 && !backward ? 1024 : 512;
     if ((v + *nv - 1) / *nv <= 32) {
@@ -633,9 +638,13 @@ cudaError_t launch(const NormArgs& a, NormShape& s, bool backward, cudaStream_t 
         cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, s.threads, smem);
         if (e != cudaSuccess) return e;
         int parts = norm_parts(s, resident);
-        // the forward starts new blocks after some 100 rows: with 139 to a thread (32768 x
-        // 5120 in 80 groups) 164 us in two turns, 176 in one; with 74 (32768 x 2560) 62.6 and 59.5
-        if (!backward) parts = norm_parts(s, resident * (1 + (int)(s.most / parts / 96)));
+        // The gated bf16 forward over narrow parts starts new blocks after 64 rows of a thread.
+        // Time against blocks that stay: 0.92 at 65536 x 5120 in 80 groups (352 us if they
+        // stay), 0.95 at 32768 x and 0.97 at 24576 x, 0.97 at 131072 x 1536 in 24, 0.98 at 16384
+        // x 5120, 1.03 at 20000 x 1440 in 40.  The others keep theirs: 1.02 to 1.04 without a gate and for wide parts (65536
+        // x 2560, 131072 x 2560, 65536 x 2048 in 16, 32768 x 4096 gated), 0.97 to 1.03 in fp32.
+        if (!backward && a.gate && a.bf16 && s.team <= 32)
+            parts = norm_parts(s, resident * (1 + (int)(s.most / parts / 64)));
         s.parts = backward && parts > s.parts ? s.parts : parts;  // (the workspace holds that many)
     }
     s.step = (long long)s.parts * s.slots;
