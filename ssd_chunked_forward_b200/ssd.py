@@ -8,8 +8,6 @@ turns torch tensors into device pointers, the current torch stream into a
 from __future__ import annotations
 
 import ctypes
-import functools
-import inspect
 import os
 
 import torch
@@ -180,33 +178,23 @@ def _torch_stream(stream, device):
     return torch.cuda.ExternalStream(handle, device=device)
 
 
-def _on_its_stream(fn):
-    """A call that allocates, with ``stream=s`` as under ``torch.cuda.stream(s)``:
-    what it allocates, clears and copies is queued on s like its kernels, and
+def _on(stream, fn, *args, **kw):
+    """fn(*args, **kw), a call that allocates, as under ``torch.cuda.stream(stream)``:
+    what it allocates, clears and copies is queued there like its kernels, and
     temporary memory goes back to that stream's pool, whose next user runs behind
     them.  New results are also marked as used by the caller's own stream, so that
     dropping them there is safe while it still reads them."""
-    at = list(inspect.signature(fn).parameters).index("stream")
-
-    @functools.wraps(fn)
-    def call(*args, **kw):
-        if len(args) > at:
-            args, stream = args[:at], args[at]
-        else:
-            stream = kw.pop("stream", None)
-        given = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)] if stream is not None else []
-        if not given or not given[0].is_cuda:  # addresses, or tensors that fn refuses
-            return fn(*args, stream=stream, **kw)
-        here, side = torch.cuda.current_stream(given[0].device), _torch_stream(stream, given[0].device)
-        with torch.cuda.stream(side):
-            out = fn(*args, **kw)
-        if side != here:
-            for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
-                if t is not None and not any(t is g for g in given):
-                    t.record_stream(here)
-        return out
-
-    return call
+    given = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)]
+    if not given or not given[0].is_cuda:  # (fn refuses them)
+        return fn(*args, **kw)
+    here, side = torch.cuda.current_stream(given[0].device), _torch_stream(stream, given[0].device)
+    with torch.cuda.stream(side):
+        out = fn(*args, **kw)
+    if side != here:
+        for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+            if t is not None and not any(t is g for g in given):
+                t.record_stream(here)
+    return out
 
 
 def _stream(stream):
@@ -267,7 +255,6 @@ def _check_inputs(x, a, Bm, Cm, D):
         raise ValueError("D must be a contiguous float32 CUDA tensor")
 
 
-@_on_its_stream
 def forward(x, a, Bm, Cm, D=None, chunk=256, *, y=None, final_state=None, want_final=True,
             workspace=None, path=PATH_AUTO, flags=0, stream=None, initial_state=None):
     """y[B,T,H,P] (and final state [B,H,N,P] fp32) of the chunked SSD forward.
@@ -277,6 +264,9 @@ def forward(x, a, Bm, Cm, D=None, chunk=256, *, y=None, final_state=None, want_f
     [B,H,N,P] float32 or None (zero).  Asynchronous on the current torch
     stream, or on ``stream``, where what it allocates then belongs too; the order
     of that stream with the inputs is the caller's, as for every call here."""
+    if stream is not None:
+        return _on(stream, forward, x, a, Bm, Cm, D, chunk, y=y, final_state=final_state, want_final=want_final,
+                   workspace=workspace, path=path, flags=flags, initial_state=initial_state)
     _check_inputs(x, a, Bm, Cm, D)
     if initial_state is not None and (initial_state.dtype != torch.float32 or not initial_state.is_cuda
                                       or not initial_state.is_contiguous()):
@@ -338,8 +328,9 @@ def device_status_where(workspace, stream=None):
     return st, line.value, block.value, thread.value
 
 
-@_on_its_stream
 def chunk_cumsum(shape: Shape, a, cum=None, stream=None):
+    if stream is not None and cum is None:
+        return _on(stream, chunk_cumsum, shape, a, None)
     nc = -(-shape.T // shape.chunk)  # the last chunk may end past T
     if cum is None:
         dims = (shape.B, shape.H, nc, shape.chunk) + ((shape.N,) if shape.a_per_state else ())
@@ -349,8 +340,9 @@ def chunk_cumsum(shape: Shape, a, cum=None, stream=None):
     return cum
 
 
-@_on_its_stream
 def chunk_state(shape: Shape, x, Bm, cum, states=None, impl=IMPL_AUTO, stream=None):
+    if stream is not None and states is None:
+        return _on(stream, chunk_state, shape, x, Bm, cum, None, impl)
     nc = -(-shape.T // shape.chunk)  # the last chunk may end past T
     if states is None:
         states = torch.empty((shape.B, shape.H, nc, shape.N, shape.P), dtype=torch.float32,
@@ -366,8 +358,9 @@ def state_pass(shape: Shape, cum, states, final_state=None, stream=None):
     return states, final_state
 
 
-@_on_its_stream
 def chunk_scan(shape: Shape, x, Bm, Cm, cum, Hin, D=None, y=None, impl=IMPL_AUTO, stream=None):
+    if stream is not None and y is None:
+        return _on(stream, chunk_scan, shape, x, Bm, Cm, cum, Hin, D, None, impl)
     if y is None:
         y = torch.empty_like(x)
     fn = load().ssd_diag_scan if shape.a_per_state else load().ssd_chunk_scan
@@ -390,10 +383,11 @@ def forward_host(shape: Shape, x_h, a_h, Bm_h, Cm_h, D_h, y_h, final_h, dev_buf,
                                    dev_buf.numel(), _stream(stream)), "ssd_forward_host")
 
 
-@_on_its_stream
 def forward_noalloc(x, a, Bm, Cm, D=None, chunk=256, *, y=None, final_state=None, stream=None):
     """The fused forward with the library's own fixed scratch (no workspace,
     nothing allocated by the library); see ssd_forward_noalloc in ssd.h."""
+    if stream is not None:
+        return _on(stream, forward_noalloc, x, a, Bm, Cm, D, chunk, y=y, final_state=final_state)
     _check_inputs(x, a, Bm, Cm, D)
     shape = shape_of(x, a, Bm, chunk)
     B, T, H, P = x.shape
@@ -408,13 +402,14 @@ def forward_noalloc(x, a, Bm, Cm, D=None, chunk=256, *, y=None, final_state=None
     return y, final_state
 
 
-@_on_its_stream
 def decode_step(x, a, Bm, Cm, D, state, *, y=None, stream=None):
     """One recurrent step for a batch of single tokens, in place on ``state``.
 
     x [B,H,P], Bm/Cm [B,G,N] (float32 or bfloat16), a [B,H] or [B,H,N] float32
     log-decays, D [H] float32 or None, state [B,H,N,P] float32 (updated).
     Returns y [B,H,P]."""
+    if stream is not None:
+        return _on(stream, decode_step, x, a, Bm, Cm, D, state, y=y)
     for name, t in (("x", x), ("a", a), ("Bm", Bm), ("Cm", Cm), ("state", state)):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
@@ -434,11 +429,12 @@ def decode_step(x, a, Bm, Cm, D, state, *, y=None, stream=None):
     return y
 
 
-@_on_its_stream
 def discretize(dt_raw, dt_bias, A_log, x, *, a_out=None, x_out=None, stream=None):
     """dt = softplus(dt_raw + dt_bias); returns (a, x_out): a = -dt exp(A_log)
     ([B,T,H], or [B,T,H,N] when A_log is [H,N]) and x_out = dt x ([B,T,H,P],
     x's dtype), the inputs of forward()."""
+    if stream is not None:
+        return _on(stream, discretize, dt_raw, dt_bias, A_log, x, a_out=a_out, x_out=x_out)
     for name, t in (("dt_raw", dt_raw), ("A_log", A_log), ("x", x)):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
@@ -457,13 +453,15 @@ def discretize(dt_raw, dt_bias, A_log, x, *, a_out=None, x_out=None, stream=None
     return a_out, x_out
 
 
-@_on_its_stream
 def forward_discretized(x, dt_raw, dt_bias, A_log, Bm, Cm, D=None, chunk=256, *, y=None, final_state=None,
                         want_final=True, workspace=None, stream=None):
     """discretize() followed by forward() in one fused pass (x_out and a are never
     written): y = SSD(dt x, -dt exp(A_log), Bm, Cm) + D (dt x), dt = softplus(dt_raw
     + dt_bias).  x [B,T,H,P] bf16, dt_raw [B,T,H] float32, dt_bias [H] or None,
     A_log [H] float32 (scalar decay only)."""
+    if stream is not None:
+        return _on(stream, forward_discretized, x, dt_raw, dt_bias, A_log, Bm, Cm, D, chunk, y=y,
+                   final_state=final_state, want_final=want_final, workspace=workspace)
     for name, t in (("dt_raw", dt_raw), ("A_log", A_log)):
         if not t.is_cuda or not t.is_contiguous() or t.dtype != torch.float32:
             raise ValueError(f"{name} must be a contiguous float32 CUDA tensor")
@@ -486,10 +484,11 @@ def forward_discretized(x, dt_raw, dt_bias, A_log, Bm, Cm, D=None, chunk=256, *,
     return y, final_state
 
 
-@_on_its_stream
 def decay_total(a, *, out=None, stream=None):
     """Total log-decay of each chain over the sequence: a [B,T,H] -> [B,H]
     (a [B,T,H,N] -> [B,H,N])."""
+    if stream is not None:
+        return _on(stream, decay_total, a, out=out)
     if not a.is_cuda or not a.is_contiguous() or a.dtype != torch.float32:
         raise ValueError("a must be a contiguous float32 CUDA tensor")
     B, T, H = a.shape[:3]
@@ -503,11 +502,12 @@ def decay_total(a, *, out=None, stream=None):
     return out
 
 
-@_on_its_stream
 def state_combine(finals, totals, h0=None, *, out=None, stream=None):
     """finals [S,B,H,N,P] (each segment's final state from zero), totals
     [S,B,H] or [S,B,H,N] -> h_in [S+1,B,H,N,P]: h_in[s] enters segment s,
     h_in[S] is the state after all of them (h0, or zero, enters segment 0)."""
+    if stream is not None:
+        return _on(stream, state_combine, finals, totals, h0, out=out)
     for name, t in (("finals", finals), ("totals", totals)):
         if not t.is_cuda or not t.is_contiguous() or t.dtype != torch.float32:
             raise ValueError(f"{name} must be a contiguous float32 CUDA tensor")
@@ -521,10 +521,12 @@ def state_combine(finals, totals, h0=None, *, out=None, stream=None):
     return out
 
 
-@_on_its_stream
 def segment_state(x, a, Bm, chunk=256, *, final_state=None, total=None, workspace=None, stream=None):
     """The state a segment builds from a zero start, [B,H,N,P] fp32, and its
     total log-decay [B,H] (or [B,H,N]), without computing its outputs."""
+    if stream is not None:
+        return _on(stream, segment_state, x, a, Bm, chunk, final_state=final_state, total=total,
+                   workspace=workspace)
     for name, t in (("x", x), ("a", a), ("Bm", Bm)):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
@@ -547,7 +549,6 @@ def backward_workspace_size(shape: Shape) -> int:
     return int(load().ssd_backward_workspace_size(ctypes.byref(shape)))
 
 
-@_on_its_stream
 def backward(x, a, Bm, Cm, D, dy, chunk=256, *, dfinal=None, initial_state=None, want_dD=True,
              want_dinit=True, workspace=None, stream=None):
     """Gradients of sum(dy * y) + <dfinal, final_state> for the forward of the
@@ -555,6 +556,9 @@ def backward(x, a, Bm, Cm, D, dy, chunk=256, *, dfinal=None, initial_state=None,
     da, dBm, dCm, dD (or None), dinit (or None).  Shapes and dtypes as for
     forward(); dy like x; dfinal and initial_state [B,H,N,P] float32 or None.  Asynchronous on the current
     torch stream (or ``stream``)."""
+    if stream is not None:
+        return _on(stream, backward, x, a, Bm, Cm, D, dy, chunk, dfinal=dfinal, initial_state=initial_state,
+                   want_dD=want_dD, want_dinit=want_dinit, workspace=workspace)
     _check_inputs(x, a, Bm, Cm, D)
     if dy.shape != x.shape or dy.dtype != x.dtype or not dy.is_contiguous():
         raise ValueError("dy must be a contiguous tensor of x's shape and dtype")
@@ -717,7 +721,6 @@ def linear_backward_workspace_size(shape: LinearShape) -> int:
     return int(load().ssd_linear_backward_workspace_size(ctypes.byref(shape)))
 
 
-@_on_its_stream
 def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqlens=None, y=None, final_state=None,
                      want_final=True, workspace=None, stream=None):
     """y and the final state of linear attention with a decay for each head:
@@ -733,6 +736,9 @@ def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqle
     start on 16-byte boundaries, other states are taken from anywhere.
     Returns y [B,T,H,V] and the state [B,H,K,V] float32 (None with
     want_final=False).  Asynchronous on the current stream of q's device."""
+    if stream is not None:
+        return _on(stream, linear_attention, q, k, v, decay, scale=scale, initial_state=initial_state,
+                   cu_seqlens=cu_seqlens, y=y, final_state=final_state, want_final=want_final, workspace=workspace)
     plan, dev = _linear_plan(q, k, v, decay, cu_seqlens), q.device
     if initial_state is not None:
         _on_device("initial_state", initial_state, dev, torch.float32, plan.state)
@@ -756,12 +762,13 @@ def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqle
     return y, final_state
 
 
-@_on_its_stream
 def linear_attention_step(q, k, v, decay, state, *, scale=None, y=None, stream=None):
     """One token of linear_attention() for a batch of sequences, in place on
     ``state`` [B,H,K,V] float32, on a 16-byte boundary: q [B,H,K], k [B,G,K],
     v [B,G,V], decay [H].
     Returns y [B,H,V]."""
+    if stream is not None:
+        return _on(stream, linear_attention_step, q, k, v, decay, state, scale=scale, y=y)
     plan, dev = _linear_plan(q, k, v, decay, None, True), q.device
     _on_device("state", state, dev, torch.float32, plan.state)
     _on_boundary("state", state, 16)
@@ -776,7 +783,6 @@ def linear_attention_step(q, k, v, decay, state, *, scale=None, y=None, stream=N
     return y
 
 
-@_on_its_stream
 def linear_attention_backward(q, k, v, decay, dy, *, scale=None, initial_state=None, dfinal=None, cu_seqlens=None,
                               want_dinit=True, workspace=None, stream=None):
     """Gradients of sum(dy * y) + <dfinal, final_state> of linear_attention()
@@ -784,6 +790,10 @@ def linear_attention_backward(q, k, v, decay, dy, *, scale=None, initial_state=N
     dv summed over the query heads of their group) and dinit ([B,H,K,V]
     float32, or None).  dy like y; dfinal like the final state, or None.  The
     decay has no gradient.  Rows outside every packed sequence come back zero."""
+    if stream is not None:
+        return _on(stream, linear_attention_backward, q, k, v, decay, dy, scale=scale,
+                   initial_state=initial_state, dfinal=dfinal, cu_seqlens=cu_seqlens, want_dinit=want_dinit,
+                   workspace=workspace)
     plan, dev = _linear_plan(q, k, v, decay, cu_seqlens), q.device
     _on_device("dy", dy, dev, q.dtype, plan.y)
     for name, t in (("initial_state", initial_state), ("dfinal", dfinal)):
@@ -860,7 +870,6 @@ def _norm_plan(x, weight, bias, groups, gate, dy=None):
     return plan
 
 
-@_on_its_stream
 def layer_norm(x, weight=None, bias=None, *, groups=1, gate=None, eps=1e-5, y=None, stream=None):
     """Layer norm over each of the ``groups`` equal parts of x's last dimension
     (groups = heads: the norm behind a sequence mixer), times silu(gate):
@@ -870,6 +879,8 @@ def layer_norm(x, weight=None, bias=None, *, groups=1, gate=None, eps=1e-5, y=No
     the last contiguous), gate the same or None, weight and bias [D] float32 or
     None.  Returns y and stats [rows, groups, 2] float32 (mean and rstd, for
     layer_norm_backward)."""
+    if stream is not None:
+        return _on(stream, layer_norm, x, weight, bias, groups=groups, gate=gate, eps=eps, y=y)
     plan, dev = _norm_plan(x, weight, bias, groups, gate), x.device
     if y is None:
         y = torch.empty(x.shape, dtype=x.dtype, device=dev)
@@ -881,12 +892,14 @@ def layer_norm(x, weight=None, bias=None, *, groups=1, gate=None, eps=1e-5, y=No
     return y, stats
 
 
-@_on_its_stream
 def layer_norm_backward(x, weight, bias, dy, stats, *, groups=1, gate=None, want_dweight=True, want_dbias=True,
                         workspace=None, stream=None):
     """Gradients of sum(dy * y) of layer_norm() for the same inputs and its
     stats: a dict of dx, dgate (None without a gate), dweight and dbias ([D]
     float32, or None)."""
+    if stream is not None:
+        return _on(stream, layer_norm_backward, x, weight, bias, dy, stats, groups=groups, gate=gate,
+                   want_dweight=want_dweight, want_dbias=want_dbias, workspace=workspace)
     plan, dev = _norm_plan(x, weight, bias, groups, gate, dy), x.device
     _on_device("stats", stats, dev, torch.float32, plan.stats)
     _on_boundary("stats", stats, 8)

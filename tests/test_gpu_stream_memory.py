@@ -97,3 +97,25 @@ def test_results_dropped_while_the_callers_stream_reads_them():
             torch.full_like(want, 7.0)
     torch.cuda.synchronize()
     assert all(torch.equal(c, want) for c in copies)
+
+
+@pytest.mark.parametrize("make,dtype,K,V", [(linear, BF, 128, 64), (norm, BF, 1536, 64)])
+def test_captured_on_a_branch(make, dtype, K, V):
+    """A call on a side stream that has joined a capture: its memory is the graph's, and
+    replays give the results again."""
+    call = make(dtype, K, V)
+    want = call(None)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        held = call(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in held.values():
+            t.fill_(7.0)
+        graph.replay()
+        junk = [torch.full((1 << n,), 0xFF, dtype=torch.uint8, device="cuda") for n in range(9, 26)]
+        torch.cuda.synchronize()
+        del junk
+        assert all(torch.equal(held[n], want[n]) for n in want)
