@@ -463,9 +463,10 @@ typedef struct {
  * for ssd_forward; not to be shared by calls that overlap in time (captured
  * graphs that replay side by side need one each).  bf16 with K, V <= 128, K
  * and V multiples of 8 and rows on 16-byte boundaries (addresses, and
- * strides multiples of 8) runs on tensor cores: the masked scores and the
+ * strides positive multiples of 8, but for dimensions of length 1) runs on
+ * tensor cores: the masked scores and the
  * state as an operand are rounded to bf16, sums and states are fp32.
- * Everything else runs on CUDA cores in fp32.  A NaN or infinity in a token
+ * Everything else runs on CUDA cores in fp32, some ten times slower.  A NaN or infinity in a token
  * reaches that token's and later outputs of its sequence, no earlier ones and
  * no other sequence's.  Asynchronous on `stream`. */
 ssd_status ssd_linear_attention(const ssd_linear_shape* shape, const void* q, const ssd_strides* q_strides,

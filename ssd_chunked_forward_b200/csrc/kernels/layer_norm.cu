@@ -23,7 +23,7 @@
 // at 255 instructions for a vector of eight numbers, which is why arithmetic goes in
 // pairs, pointers move along, and a thread takes more than one vector.
 // Now: 32768 x 2560 forward 59.5 us (5.6 TB/s), backward 97 (5.2); 32768 x 5120 in 80
-// groups with gate 164 (6.1) and 325 (5.2).  Elements of 2 bytes, which cp.async cannot copy, are
+// groups with gate 164 (6.1) and 312 (5.4).  Elements of 2 bytes, which cp.async cannot copy, are
 // prefetched one row ahead in registers.
 #include <type_traits>
 

@@ -14,8 +14,8 @@
 //
 // Bound by the fp32 pipes and the shared-memory reads that feed them; short calls
 // by the latency of a chunk (some 4 us). Measured, fp32: 4 x 2048 tokens, 16 heads,
-// 64 x 128 566 us (gradients 1450); 2 x 333 tokens, 8 query and 2 key heads, 48 x 64
-// 33 (gradients 55).
+// 64 x 128 567 us (gradients 1460); 2 x 333 tokens, 8 query and 2 key heads, 48 x 64
+// 33 (gradients 54); bf16, 8 x 700 tokens, 24 heads, 100 x 100 607 (gradients 1504).
 #include "../common.cuh"
 #include "../debug_checks.cuh"
 #include "../linear.h"

@@ -40,9 +40,9 @@
 // With V = 128 the lanes of Z are the state's columns (v), else its rows (k): an
 // MMA takes 128 rows, and the other order would waste half of them.
 //
-// Measured (148 chains of 8192 tokens, a chain per SM, final state wanted; in brackets
-// what their bytes take at the copy rate): 128 x 64 187 us (142), 64 x 64 176 (95),
-// 64 x 128 220 (142), 128 x 128 355 (190); without the state 5 to 10 % less.  What
+// Measured (4 x 8192 tokens, 37 heads: a chain per SM; with the final state, without
+// it, and in brackets what the bytes take at the copy rate): 128 x 64 178, 164 us (142),
+// 64 x 64 153, 139 (95), 64 x 128 190, 181 (142), 128 x 128 302, 283 (190).  What
 // bounds it is the chain of dependent products of a chunk; no unit is busy for more
 // than half of the time.
 #include <climits>

@@ -734,8 +734,13 @@ def linear_attention(q, k, v, decay, *, scale=None, initial_state=None, cu_seqle
     [S,H,K,V]; rows of a given y outside every sequence stay as they are (those
     of a new y are not set).  A given y and final_state (which may be initial_state)
     start on 16-byte boundaries, other states are taken from anywhere.
+    bfloat16 with K and V up to 128 and multiples of 8, and rows on 16-byte
+    boundaries (no stride of 0), runs on tensor cores; other calls run on CUDA
+    cores, some ten times slower.
     Returns y [B,T,H,V] and the state [B,H,K,V] float32 (None with
-    want_final=False).  Asynchronous on the current stream of q's device."""
+    want_final=False).  Asynchronous on the current stream of q's device; a kernel's
+    wait that gave up leaves y undefined and says so in the workspace, if the caller
+    gives one to ask (device_status)."""
     if stream is not None:
         return _on(stream, linear_attention, q, k, v, decay, scale=scale, initial_state=initial_state,
                    cu_seqlens=cu_seqlens, y=y, final_state=final_state, want_final=want_final, workspace=workspace)
